@@ -346,6 +346,138 @@ KDA_API size_t kda_chunk_bwd_chunkwise_workspace_size(int64_t total_tokens, int3
 KDA_API size_t kda_chunk_bwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t d_k,
                                             int32_t d_v);
 
+/*
+ * The operators of a state-space layer, from here to kda_layer_norm_bwd (no counterpart in the pages):
+ * scan, short convolution and norm, for prompts, single tokens and gradients.  Their activations and
+ * states need only their own type's alignment; where all of a call's are 16-byte aligned and rows hold
+ * whole vectors, they are moved as vectors.  Workspaces are 16-byte aligned.
+ *
+ * Selective state space scan: the recurrence of a state-space layer, beside the gated delta rule.  Per channel c of D with n states, in group g = c / (D / G):
+ *   delta_t = softplus(dt_t + dt_bias),  A = -exp(A_log)
+ *   h_t[m]  = exp(delta_t A[m]) h_{t-1}[m] + delta_t u_t B_t[g][m]
+ *   out_t   = silu(z_t) (sum_m C_t[g][m] h_t[m] + skip u_t)
+ *
+ * kda_selective_scan_fwd -- packed variable-length sequences (cu_seqlens as kda_chunk_fwd).
+ *   u, dt   [total_tokens, D]      input and step logits, of `dtype` (bf16 or fp32)
+ *   B, C    [total_tokens, G, n]   of `dtype`; G divides D, 1 <= n <= 64
+ *   z       [total_tokens, D] gate logits of `dtype`, or NULL for no gate
+ *   A_log   fp32 [D, n]; skip, dt_bias fp32 [D], each may be NULL (zero)
+ *   initial_state fp32 [num_seqs, D, n] or NULL (zeros); final_state fp32 [num_seqs, D, n] or NULL (not
+ *     written); final_state may be initial_state, but not overlap it otherwise
+ *   out     [total_tokens, D] of `dtype`; it overlaps no input
+ *   workspace: kda_selective_scan_fwd_workspace_size(...) bytes (0 when sequences are not cut), 16-byte
+ *     aligned; needs no initialisation.
+ * States, decays and sums are fp32.  Where channels and sequences alone would leave the GPU empty, long
+ * sequences are cut into segments (a second launch); results then differ from the uncut ones in the
+ * last bits.  Deterministic.  Zero-length sequences copy their initial state (or zeros) to final_state.
+ */
+KDA_API kda_status kda_selective_scan_fwd(const void *u, const void *dt, const float *A_log, const void *B,
+                                          const void *C, const float *skip, const void *z, const float *dt_bias,
+                                          const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                          int32_t D, int32_t n, int32_t G, const float *initial_state,
+                                          float *final_state, void *out, kda_dtype dtype, void *workspace,
+                                          size_t workspace_bytes, void *stream);
+
+/* Workspace of kda_selective_scan_fwd (host-only; 0 on invalid sizes, or when none is needed). */
+KDA_API size_t kda_selective_scan_fwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t D, int32_t n,
+                                                     int32_t G);
+
+/*
+ * kda_selective_scan_step -- one token for N independent states, in place.
+ *   u, dt, z, out [N, D]; B, C [N, G, n] of `dtype`; state fp32 [N, D, n] read and overwritten; the rest as
+ *   kda_selective_scan_fwd.  out overlaps no input.
+ */
+KDA_API kda_status kda_selective_scan_step(const void *u, const void *dt, const float *A_log, const void *B,
+                                           const void *C, const float *skip, const void *z, const float *dt_bias,
+                                           float *state, void *out, kda_dtype dtype, int32_t N, int32_t D, int32_t n,
+                                           int32_t G, void *stream);
+
+/*
+ * kda_selective_scan_bwd -- gradients of kda_selective_scan_fwd with the same inputs, given dout (of `dtype`, the
+ * gradient of out) and optionally dfinal_state (fp32).  Nothing of the forward pass is needed.
+ *   du, ddt, dz [total_tokens, D] and dB, dC [total_tokens, G, n] of `dtype`, each rounded once; dz is required
+ *   when z is given; dA_log fp32 [D, n]; dskip, ddt_bias fp32 [D], each may be NULL (not written);
+ *   dinitial_state fp32 [num_seqs, D, n] or NULL.  All are overwritten; no output overlaps an input or
+ *   another output.
+ *   workspace: kda_selective_scan_bwd_workspace_size(...) bytes, 16-byte aligned, no initialisation: two states of
+ *   every chunk of 16 ceil(n / 4) tokens (a power of two from 16 to 64) and the channel blocks' shares of dB and dC.
+ * Deterministic.
+ */
+KDA_API kda_status kda_selective_scan_bwd(const void *u, const void *dt, const float *A_log, const void *B,
+                                          const void *C, const float *skip, const void *z, const float *dt_bias,
+                                          const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                          int32_t D, int32_t n, int32_t G, const float *initial_state,
+                                          const void *dout, const float *dfinal_state, void *du, void *ddt,
+                                          float *dA_log, void *dB, void *dC, float *dskip, void *dz, float *ddt_bias,
+                                          float *dinitial_state, kda_dtype dtype, void *workspace,
+                                          size_t workspace_bytes, void *stream);
+
+/* Workspace of kda_selective_scan_bwd (host-only; 0 on invalid sizes). */
+KDA_API size_t kda_selective_scan_bwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t D, int32_t n,
+                                                     int32_t G);
+
+/*
+ * kda_short_conv_fwd -- kda_short_conv with what a layer needs to be served and trained: a carried
+ * window, a bias, SiLU, either storage type and any head size.
+ *   p_t[h][c] = bias[h][c] + sum_{j < width} w[h][c][j] x_{t-(width-1)+j}[h][c]
+ *   s = silu != 0 ? p / (1 + exp(-p)) : p;   y_t[h] = l2norm != 0 ? s / sqrt(|s|^2 + 1e-12) : s
+ *   x, y  [total_tokens, H, d] of `dtype`, not overlapping; d = 64 or 128 with l2norm, else any
+ *   w fp32 [H, d, width], 1 <= width <= 4; bias fp32 [H, d] or NULL
+ *   initial_state [num_seqs, width - 1, H, d] of `dtype` or NULL (zeros): the last inputs before each
+ *     sequence, oldest first; final_state likewise, the last inputs of each sequence (of its initial state
+ *     and tokens together), or NULL; it may be initial_state, but not overlap it otherwise.
+ */
+KDA_API kda_status kda_short_conv_fwd(const void *x, const float *w, const float *bias, const int32_t *cu_seqlens,
+                                      int32_t num_seqs, int64_t total_tokens, int32_t H, int32_t d, int32_t width,
+                                      int32_t silu, int32_t l2norm, const void *initial_state, void *final_state,
+                                      void *y, kda_dtype dtype, void *stream);
+
+/*
+ * kda_short_conv_step -- one token of N sequences: x, y [N, H, d]; state [N, width - 1, H, d] is read and
+ * overwritten (may be NULL when width is 1); the rest as kda_short_conv_fwd.  y overlaps neither x nor state.
+ */
+KDA_API kda_status kda_short_conv_step(const void *x, const float *w, const float *bias, void *state, int32_t N,
+                                       int32_t H, int32_t d, int32_t width, int32_t silu, int32_t l2norm, void *y,
+                                       kda_dtype dtype, void *stream);
+
+/*
+ * kda_short_conv_bwd -- gradients of kda_short_conv_fwd with the same inputs, given dy and optionally dfinal_state
+ * (both of `dtype`).  dx [total_tokens, H, d] and dinitial_state [num_seqs, width - 1, H, d] (or NULL) of `dtype`;
+ * dw fp32 [H, d, width]; dbias fp32 [H, d] or NULL.  dx overlaps neither x nor dy.
+ *   workspace: kda_short_conv_bwd_workspace_size(...) bytes, 16-byte aligned (shares of dw and dbias of runs of
+ *   tokens, added in a fixed order: deterministic).
+ */
+KDA_API kda_status kda_short_conv_bwd(const void *x, const float *w, const float *bias, const int32_t *cu_seqlens,
+                                      int32_t num_seqs, int64_t total_tokens, int32_t H, int32_t d, int32_t width,
+                                      int32_t silu, int32_t l2norm, const void *initial_state, const void *dy,
+                                      const void *dfinal_state, void *dx, float *dw, float *dbias,
+                                      void *dinitial_state, kda_dtype dtype, void *workspace, size_t workspace_bytes,
+                                      void *stream);
+
+/* Workspace of kda_short_conv_bwd (host-only; 0 on invalid sizes). */
+KDA_API size_t kda_short_conv_bwd_workspace_size(int64_t total_tokens, int32_t H, int32_t d, int32_t width);
+
+/*
+ * kda_layer_norm_fwd -- y = (x - mean) rstd w + b over rows of d columns, rstd = 1 / sqrt(var + eps).
+ *   x, y [rows, d] of `dtype`, not overlapping; w fp32 [d]; b fp32 [d] or NULL; mean, rstd fp32 [rows], each
+ *   may be NULL (not written).  1 <= d <= 16384.
+ */
+KDA_API kda_status kda_layer_norm_fwd(const void *x, const float *w, const float *b, int64_t rows, int32_t d, float eps,
+                                      void *y, float *mean, float *rstd, kda_dtype dtype, void *stream);
+
+/*
+ * kda_layer_norm_bwd -- gradients of kda_layer_norm_fwd: x and w as there, mean and rstd as it wrote them, dy of
+ * `dtype`.  dx [rows, d] of `dtype`, overlapping neither x nor dy; dw fp32 [d]; db fp32 [d] or NULL.
+ *   workspace: kda_layer_norm_bwd_workspace_size(...) bytes, 16-byte aligned (shares of dw and db, added in a
+ *   fixed order: deterministic).
+ */
+KDA_API kda_status kda_layer_norm_bwd(const void *x, const float *w, const float *mean, const float *rstd, const void *dy,
+                                      int64_t rows, int32_t d, void *dx, float *dw, float *db, kda_dtype dtype,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace of kda_layer_norm_bwd (host-only; 0 on invalid sizes). */
+KDA_API size_t kda_layer_norm_bwd_workspace_size(int64_t rows, int32_t d);
+
 /* Static description of a status code. */
 KDA_API const char *kda_status_string(kda_status status);
 

@@ -18,6 +18,10 @@ Entry points (same names as the C ABI):
                                                             chunkwise form, kda_chunk_bwd_chunkwise)
   chunk_kda(...)                                            the prefill as a torch.autograd function: its
                                                             forward is kda_chunk_fwd, its backward kda_chunk_bwd
+  kda_selective_scan_fwd / _step / _bwd, selective_scan     a state-space layer's scan: prompts, single tokens,
+                                                            gradients, and as an autograd function
+  kda_short_conv_fwd / _step / _bwd, short_conv             the short convolution with its carried window
+  kda_layer_norm_fwd / _bwd, layer_norm                     layer norm
 """
 from __future__ import annotations
 
@@ -35,6 +39,11 @@ __all__ = ["kda_chunk_fwd", "kda_decode_step", "kda_chunk_fwd_workspace_size",
            "kda_state_combine", "kda_segment_maps", "context_parallel_states", "kda_context_parallel_fwd",
            "kda_chunk_bwd", "kda_chunk_bwd_workspace_size", "kda_chunk_fwd_host",
            "kda_chunk_fwd_host_buffer_size", "chunk_kda",
+           "kda_selective_scan_fwd", "kda_selective_scan_fwd_workspace_size", "kda_selective_scan_step",
+           "kda_selective_scan_bwd", "kda_selective_scan_bwd_workspace_size", "selective_scan",
+           "kda_short_conv_fwd", "kda_short_conv_step", "kda_short_conv_bwd", "kda_short_conv_bwd_workspace_size",
+           "short_conv", "kda_layer_norm_fwd", "kda_layer_norm_bwd", "kda_layer_norm_bwd_workspace_size",
+           "layer_norm",
            "LIB_PATH", "lib"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
@@ -114,6 +123,34 @@ def _load() -> ctypes.CDLL:
     L.kda_segment_maps.restype = ctypes.c_int
     L.kda_segment_maps_workspace_size.argtypes = [i64, i32, i32, i32]
     L.kda_segment_maps_workspace_size.restype = sz
+    dtype = ctypes.c_int
+    L.kda_selective_scan_fwd.argtypes = [vp, vp, fp, vp, vp, fp, vp, fp, vp, i32, i64, i32, i32, i32, fp, fp, vp,
+                                         dtype, vp, sz, vp]
+    L.kda_selective_scan_fwd.restype = ctypes.c_int
+    L.kda_selective_scan_fwd_workspace_size.argtypes = [i64, i32, i32, i32, i32]
+    L.kda_selective_scan_fwd_workspace_size.restype = sz
+    L.kda_selective_scan_step.argtypes = [vp, vp, fp, vp, vp, fp, vp, fp, fp, vp, dtype, i32, i32, i32, i32, vp]
+    L.kda_selective_scan_step.restype = ctypes.c_int
+    L.kda_selective_scan_bwd.argtypes = [vp, vp, fp, vp, vp, fp, vp, fp, vp, i32, i64, i32, i32, i32, fp, vp, fp,
+                                         vp, vp, fp, vp, vp, fp, vp, fp, fp, dtype, vp, sz, vp]
+    L.kda_selective_scan_bwd.restype = ctypes.c_int
+    L.kda_selective_scan_bwd_workspace_size.argtypes = [i64, i32, i32, i32, i32]
+    L.kda_selective_scan_bwd_workspace_size.restype = sz
+    L.kda_short_conv_fwd.argtypes = [vp, fp, fp, vp, i32, i64, i32, i32, i32, i32, i32, vp, vp, vp, dtype, vp]
+    L.kda_short_conv_fwd.restype = ctypes.c_int
+    L.kda_short_conv_step.argtypes = [vp, fp, fp, vp, i32, i32, i32, i32, i32, i32, vp, dtype, vp]
+    L.kda_short_conv_step.restype = ctypes.c_int
+    L.kda_short_conv_bwd.argtypes = [vp, fp, fp, vp, i32, i64, i32, i32, i32, i32, i32, vp, vp, vp, vp, fp, fp, vp,
+                                     dtype, vp, sz, vp]
+    L.kda_short_conv_bwd.restype = ctypes.c_int
+    L.kda_short_conv_bwd_workspace_size.argtypes = [i64, i32, i32, i32]
+    L.kda_short_conv_bwd_workspace_size.restype = sz
+    L.kda_layer_norm_fwd.argtypes = [vp, fp, fp, i64, i32, f32, vp, fp, fp, dtype, vp]
+    L.kda_layer_norm_fwd.restype = ctypes.c_int
+    L.kda_layer_norm_bwd.argtypes = [vp, fp, fp, fp, vp, i64, i32, vp, fp, fp, dtype, vp, sz, vp]
+    L.kda_layer_norm_bwd.restype = ctypes.c_int
+    L.kda_layer_norm_bwd_workspace_size.argtypes = [i64, i32]
+    L.kda_layer_norm_bwd_workspace_size.restype = sz
     return L
 
 
@@ -615,6 +652,367 @@ def chunk_kda(q, k, v, a, beta, A_log, cu_seqlens, gate=None, initial_state=None
     initial_state.  Returns (out [T, H, d_v], final_state [N, H, d_k, d_v] fp32); a loss on either
     or both reaches the inputs through kda_chunk_bwd."""
     return _ChunkKDA.apply(q, k, v, a, beta, A_log, gate, initial_state, cu_seqlens, float(scale), out_dtype)
+
+
+# ---- the selective scan, the convolution with its carried window, layer norm ---------------------
+
+
+class _Call:
+    """Where a call's work runs: its device is made current, and what it allocates belongs to its stream."""
+
+    def __init__(self, x, stream):
+        if not x.is_cuda:
+            raise ValueError(f"tensors must be on a CUDA device, got {x.device}")
+        self.device, self.stream, self._with = x.device, stream, []
+        if x.device.index != torch.cuda.current_device():
+            self._with.append(torch.cuda.device(x.device))
+        if stream is not None:
+            if stream.device != x.device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+            self._with.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for w in self._with:
+            w.__enter__()
+        self.handle = _stream_handle(self.stream, self.device)
+        return self
+
+    def __exit__(self, *exc):
+        for w in reversed(self._with):
+            w.__exit__(*exc)
+
+    def empty(self, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, given, nbytes):
+        if given is None:
+            return (torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None), nbytes
+        if given.device != self.device or not given.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {self.device}")
+        return given, given.numel() * given.element_size()
+
+
+def _io_dtype(x, name):
+    if x.dtype not in _OUT_DTYPES:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {x.dtype}")
+    return _OUT_DTYPES[x.dtype]
+
+
+def _scan_args(u, dt, A_log, B, C, skip, z, dt_bias):
+    """Checks what the scan's calls share; returns (rows, D, n, G, dtype code)."""
+    code = _io_dtype(u, "u")
+    if u.dim() != 2 or B.dim() != 3 or A_log.dim() != 2:
+        raise ValueError("u must be [tokens, D], B [tokens, G, n] and A_log [D, n]")
+    rows, D = u.shape
+    G, n = B.shape[1:]
+    dev, t, f32 = u.device, u.dtype, torch.float32
+    _need(u, "u", t, (rows, D), dev)
+    _need(dt, "dt", t, (rows, D), dev)
+    _need(A_log, "A_log", f32, (D, n), dev)
+    _need(B, "B", t, (rows, G, n), dev)
+    _need(C, "C", t, (rows, G, n), dev)
+    if z is not None:
+        _need(z, "z", t, (rows, D), dev)
+    if skip is not None:
+        _need(skip, "skip", f32, (D,), dev)
+    if dt_bias is not None:
+        _need(dt_bias, "dt_bias", f32, (D,), dev)
+    return rows, D, n, G, code
+
+
+def _need_seqlens(cu_seqlens, dev):
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be int32 [num_seqs + 1]")
+    _need(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, dev)
+    return cu_seqlens.numel() - 1
+
+
+def kda_selective_scan_fwd_workspace_size(total_tokens, num_seqs, D, n, G=1) -> int:
+    return int(lib.kda_selective_scan_fwd_workspace_size(total_tokens, num_seqs, D, n, G))
+
+
+def kda_selective_scan_bwd_workspace_size(total_tokens, num_seqs, D, n, G=1) -> int:
+    return int(lib.kda_selective_scan_bwd_workspace_size(total_tokens, num_seqs, D, n, G))
+
+
+def kda_selective_scan_fwd(u, dt, A_log, B, C, cu_seqlens, skip=None, z=None, dt_bias=None, initial_state=None,
+                           output_final_state: bool = True, out=None, final_state=None, workspace=None, stream=None):
+    """Selective state space scan over packed sequences (see include/kda.h):
+    h_t = exp(delta A) h_{t-1} + delta u B_t, out_t = silu(z) (C_t h_t + skip u), delta = softplus(dt + dt_bias),
+    A = -exp(A_log).
+
+    u, dt, z [T, D] and B, C [T, G, n], all bfloat16 or all float32; A_log fp32 [D, n]; skip, dt_bias fp32
+    [D] or None; cu_seqlens int32 [N + 1] (device); initial_state fp32 [N, D, n] or None; final_state may
+    be initial_state.  Returns (out [T, D], final_state fp32 [N, D, n] or None)."""
+    T, D, n, G, code = _scan_args(u, dt, A_log, B, C, skip, z, dt_bias)
+    N = _need_seqlens(cu_seqlens, u.device)
+    f32 = torch.float32
+    if initial_state is not None:
+        _need(initial_state, "initial_state", f32, (N, D, n), u.device)
+    with _Call(u, stream) as call:
+        if out is None:
+            out = call.empty((T, D), u.dtype)
+        _need(out, "out", u.dtype, (T, D), u.device)
+        if final_state is None and output_final_state:
+            final_state = call.empty((N, D, n), f32)
+        if final_state is not None:
+            _need(final_state, "final_state", f32, (N, D, n), u.device)
+        ws, ws_bytes = call.workspace(workspace, kda_selective_scan_fwd_workspace_size(T, N, D, n, G))
+        st = lib.kda_selective_scan_fwd(_ptr(u), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(skip), _ptr(z),
+                                        _ptr(dt_bias), _ptr(cu_seqlens), N, T, D, n, G, _ptr(initial_state),
+                                        _ptr(final_state), _ptr(out), code, _ptr(ws), ws_bytes, call.handle)
+    _check(st, "kda_selective_scan_fwd")
+    return out, final_state
+
+
+def kda_selective_scan_step(u, dt, A_log, B, C, state, skip=None, z=None, dt_bias=None, out=None, stream=None):
+    """One token of N sequences; ``state`` fp32 [N, D, n] is updated in place.  u, dt, z [N, D]; B, C
+    [N, G, n]; the rest as kda_selective_scan_fwd.  Returns out [N, D]."""
+    N, D, n, G, code = _scan_args(u, dt, A_log, B, C, skip, z, dt_bias)
+    _need(state, "state", torch.float32, (N, D, n), u.device)
+    with _Call(u, stream) as call:
+        if out is None:
+            out = call.empty((N, D), u.dtype)
+        _need(out, "out", u.dtype, (N, D), u.device)
+        st = lib.kda_selective_scan_step(_ptr(u), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(skip), _ptr(z),
+                                         _ptr(dt_bias), _ptr(state), _ptr(out), code, N, D, n, G, call.handle)
+    _check(st, "kda_selective_scan_step")
+    return out
+
+
+def kda_selective_scan_bwd(u, dt, A_log, B, C, cu_seqlens, dout, skip=None, z=None, dt_bias=None, initial_state=None,
+                           dfinal_state=None, workspace=None, stream=None):
+    """Gradients of kda_selective_scan_fwd with the same inputs.  dout of u's dtype [T, D]; dfinal_state fp32
+    [N, D, n] or None.  Returns a dict: du, ddt, dz [T, D] and dB, dC [T, G, n] of u's dtype; dA_log [D, n],
+    dskip, ddt_bias [D], dinitial_state [N, D, n] fp32; None for what was not given."""
+    T, D, n, G, code = _scan_args(u, dt, A_log, B, C, skip, z, dt_bias)
+    N = _need_seqlens(cu_seqlens, u.device)
+    f32, t, dev = torch.float32, u.dtype, u.device
+    _need(dout, "dout", t, (T, D), dev)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", f32, (N, D, n), dev)
+    if dfinal_state is not None:
+        _need(dfinal_state, "dfinal_state", f32, (N, D, n), dev)
+    with _Call(u, stream) as call:
+        given = lambda x, shape, dtype: None if x is None else call.empty(shape, dtype)  # noqa: E731
+        g = dict(du=call.empty((T, D), t), ddt=call.empty((T, D), t), dA_log=call.empty((D, n), f32),
+                 dB=call.empty((T, G, n), t), dC=call.empty((T, G, n), t), dskip=given(skip, (D,), f32),
+                 dz=given(z, (T, D), t), ddt_bias=given(dt_bias, (D,), f32),
+                 dinitial_state=given(initial_state, (N, D, n), f32))
+        ws, ws_bytes = call.workspace(workspace, kda_selective_scan_bwd_workspace_size(T, N, D, n, G))
+        st = lib.kda_selective_scan_bwd(_ptr(u), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(skip), _ptr(z),
+                                        _ptr(dt_bias), _ptr(cu_seqlens), N, T, D, n, G, _ptr(initial_state),
+                                        _ptr(dout), _ptr(dfinal_state), _ptr(g["du"]), _ptr(g["ddt"]),
+                                        _ptr(g["dA_log"]), _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dskip"]),
+                                        _ptr(g["dz"]), _ptr(g["ddt_bias"]), _ptr(g["dinitial_state"]), code, _ptr(ws),
+                                        ws_bytes, call.handle)
+    _check(st, "kda_selective_scan_bwd")
+    return g
+
+
+def _conv_args(x, w, bias):
+    code = _io_dtype(x, "x")
+    if x.dim() != 3 or w.dim() != 3:
+        raise ValueError("x must be [tokens, H, d] and w [H, d, width]")
+    rows, H, d = x.shape
+    W = w.shape[2]
+    _need(x, "x", x.dtype, (rows, H, d), x.device)
+    _need(w, "w", torch.float32, (H, d, W), x.device)
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (H, d), x.device)
+    return rows, H, d, W, code
+
+
+def kda_short_conv_fwd(x, w, cu_seqlens, bias=None, initial_state=None, silu: bool = False, l2norm: bool = False,
+                       output_final_state: bool = True, out=None, final_state=None, stream=None):
+    """Causal depthwise convolution over packed sequences with its carried window (see include/kda.h):
+    bias + sum_j w[..., j] x_{t-(width-1)+j}, then SiLU, then L2 normalisation per head, each optional.
+
+    x [T, H, d] bfloat16 or float32; w fp32 [H, d, width], width <= 4; bias fp32 [H, d] or None;
+    initial_state [N, width - 1, H, d] of x's dtype or None: the inputs before each sequence, oldest first;
+    final_state likewise (it may be initial_state).  Returns (y [T, H, d], final_state or None)."""
+    T, H, d, W, code = _conv_args(x, w, bias)
+    N = _need_seqlens(cu_seqlens, x.device)
+    state = (N, W - 1, H, d)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", x.dtype, state, x.device)
+    with _Call(x, stream) as call:
+        if out is None:
+            out = call.empty((T, H, d), x.dtype)
+        _need(out, "out", x.dtype, (T, H, d), x.device)
+        if final_state is None and output_final_state:
+            final_state = call.empty(state, x.dtype)
+        if final_state is not None:
+            _need(final_state, "final_state", x.dtype, state, x.device)
+        st = lib.kda_short_conv_fwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(cu_seqlens), N, T, H, d, W, int(silu), int(l2norm),
+                                    _ptr(initial_state), _ptr(final_state), _ptr(out), code, call.handle)
+    _check(st, "kda_short_conv_fwd")
+    return out, final_state
+
+
+def kda_short_conv_step(x, w, state, bias=None, silu: bool = False, l2norm: bool = False, out=None, stream=None):
+    """One token of N sequences: x [N, H, d]; ``state`` [N, width - 1, H, d] of x's dtype is updated in
+    place.  The rest as kda_short_conv_fwd.  Returns y [N, H, d]."""
+    N, H, d, W, code = _conv_args(x, w, bias)
+    _need(state, "state", x.dtype, (N, W - 1, H, d), x.device)
+    with _Call(x, stream) as call:
+        if out is None:
+            out = call.empty((N, H, d), x.dtype)
+        _need(out, "out", x.dtype, (N, H, d), x.device)
+        st = lib.kda_short_conv_step(_ptr(x), _ptr(w), _ptr(bias), _ptr(state), N, H, d, W, int(silu), int(l2norm),
+                                     _ptr(out), code, call.handle)
+    _check(st, "kda_short_conv_step")
+    return out
+
+
+def kda_short_conv_bwd_workspace_size(total_tokens, H, d, width) -> int:
+    return int(lib.kda_short_conv_bwd_workspace_size(total_tokens, H, d, width))
+
+
+def kda_short_conv_bwd(x, w, cu_seqlens, dy, bias=None, initial_state=None, dfinal_state=None, silu: bool = False,
+                       l2norm: bool = False, workspace=None, stream=None):
+    """Gradients of kda_short_conv_fwd with the same inputs; dy [T, H, d] and dfinal_state (or None) of x's
+    dtype.  Returns a dict: dx and dinitial_state of x's dtype, dw [H, d, width] and dbias [H, d] fp32; None
+    for what was not given."""
+    T, H, d, W, code = _conv_args(x, w, bias)
+    N = _need_seqlens(cu_seqlens, x.device)
+    state, t, f32 = (N, W - 1, H, d), x.dtype, torch.float32
+    _need(dy, "dy", t, (T, H, d), x.device)
+    for name, s in (("initial_state", initial_state), ("dfinal_state", dfinal_state)):
+        if s is not None:
+            _need(s, name, t, state, x.device)
+    with _Call(x, stream) as call:
+        g = dict(dx=call.empty((T, H, d), t), dw=call.empty((H, d, W), f32),
+                 dbias=None if bias is None else call.empty((H, d), f32),
+                 dinitial_state=None if initial_state is None else call.empty(state, t))
+        ws, ws_bytes = call.workspace(workspace, kda_short_conv_bwd_workspace_size(T, H, d, W))
+        st = lib.kda_short_conv_bwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(cu_seqlens), N, T, H, d, W, int(silu), int(l2norm),
+                                    _ptr(initial_state), _ptr(dy), _ptr(dfinal_state), _ptr(g["dx"]), _ptr(g["dw"]),
+                                    _ptr(g["dbias"]), _ptr(g["dinitial_state"]), code, _ptr(ws), ws_bytes, call.handle)
+    _check(st, "kda_short_conv_bwd")
+    return g
+
+
+def kda_layer_norm_bwd_workspace_size(rows, d) -> int:
+    return int(lib.kda_layer_norm_bwd_workspace_size(rows, d))
+
+
+def kda_layer_norm_fwd(x, w, b=None, eps: float = 1e-5, out=None, stream=None):
+    """Layer norm over the last dimension (up to 16384): y = (x - mean) rstd w + b.  x [..., d] bfloat16 or
+    float32; w, b fp32 [d] (b may be None).  Returns (y, mean, rstd), mean and rstd fp32 [...]."""
+    code = _io_dtype(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    d, lead = x.shape[-1], x.shape[:-1]
+    rows = x.numel() // d if d else 0
+    _need(x, "x", x.dtype, x.shape, x.device)
+    _need(w, "w", torch.float32, (d,), x.device)
+    if b is not None:
+        _need(b, "b", torch.float32, (d,), x.device)
+    with _Call(x, stream) as call:
+        if out is None:
+            out = call.empty(x.shape, x.dtype)
+        _need(out, "out", x.dtype, x.shape, x.device)
+        mean, rstd = call.empty(lead, torch.float32), call.empty(lead, torch.float32)
+        st = lib.kda_layer_norm_fwd(_ptr(x), _ptr(w), _ptr(b), rows, d, float(eps), _ptr(out), _ptr(mean), _ptr(rstd),
+                                    code, call.handle)
+    _check(st, "kda_layer_norm_fwd")
+    return out, mean, rstd
+
+
+def kda_layer_norm_bwd(x, w, mean, rstd, dy, has_bias: bool = True, workspace=None, stream=None):
+    """Gradients of kda_layer_norm_fwd; mean and rstd are the ones it returned, dy of x's dtype.  Returns a
+    dict: dx of x's dtype, dw and (with has_bias, else None) dbias fp32 [d]."""
+    code = _io_dtype(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    d, lead = x.shape[-1], x.shape[:-1]
+    rows = x.numel() // d if d else 0
+    _need(x, "x", x.dtype, x.shape, x.device)
+    _need(dy, "dy", x.dtype, x.shape, x.device)
+    _need(w, "w", torch.float32, (d,), x.device)
+    _need(mean, "mean", torch.float32, lead, x.device)
+    _need(rstd, "rstd", torch.float32, lead, x.device)
+    with _Call(x, stream) as call:
+        g = dict(dx=call.empty(x.shape, x.dtype), dw=call.empty((d,), torch.float32),
+                 dbias=call.empty((d,), torch.float32) if has_bias else None)
+        ws, ws_bytes = call.workspace(workspace, kda_layer_norm_bwd_workspace_size(rows, d))
+        st = lib.kda_layer_norm_bwd(_ptr(x), _ptr(w), _ptr(mean), _ptr(rstd), _ptr(dy), rows, d, _ptr(g["dx"]),
+                                    _ptr(g["dw"]), _ptr(g["dbias"]), code, _ptr(ws), ws_bytes, call.handle)
+    _check(st, "kda_layer_norm_bwd")
+    return g
+
+
+def _grad(d, like):
+    """An incoming gradient as the kernels take it: of its tensor's dtype, dense; zeros where there is none."""
+    return torch.zeros_like(like) if d is None else d.to(like.dtype).contiguous()
+
+
+class _SelectiveScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, u, dt, A_log, B, C, skip, z, dt_bias, initial_state, cu_seqlens):
+        out, last = kda_selective_scan_fwd(u, dt, A_log, B, C, cu_seqlens, skip=skip, z=z, dt_bias=dt_bias,
+                                           initial_state=initial_state)
+        ctx.save_for_backward(u, dt, A_log, B, C, skip, z, dt_bias, initial_state, cu_seqlens)
+        ctx.set_materialize_grads(False)
+        return out, last
+
+    @staticmethod
+    def backward(ctx, dout, dlast):
+        u, dt, A_log, B, C, skip, z, dt_bias, initial_state, cu_seqlens = ctx.saved_tensors
+        g = kda_selective_scan_bwd(u, dt, A_log, B, C, cu_seqlens, _grad(dout, u), skip=skip, z=z, dt_bias=dt_bias,
+                                   initial_state=initial_state, dfinal_state=None if dlast is None else dlast.contiguous())
+        return (g["du"], g["ddt"], g["dA_log"], g["dB"], g["dC"], g["dskip"], g["dz"], g["ddt_bias"],
+                g["dinitial_state"], None)
+
+
+def selective_scan(u, dt, A_log, B, C, cu_seqlens, skip=None, z=None, dt_bias=None, initial_state=None):
+    """kda_selective_scan_fwd as a differentiable function of every tensor but cu_seqlens; its backward is
+    kda_selective_scan_bwd.  Returns (out, final_state)."""
+    return _SelectiveScan.apply(u, dt, A_log, B, C, skip, z, dt_bias, initial_state, cu_seqlens)
+
+
+class _ShortConv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, initial_state, cu_seqlens, silu, l2norm):
+        y, last = kda_short_conv_fwd(x, w, cu_seqlens, bias=bias, initial_state=initial_state, silu=silu, l2norm=l2norm)
+        ctx.save_for_backward(x, w, bias, initial_state, cu_seqlens)
+        ctx.silu, ctx.l2norm = silu, l2norm
+        ctx.set_materialize_grads(False)
+        return y, last
+
+    @staticmethod
+    def backward(ctx, dy, dlast):
+        x, w, bias, initial_state, cu_seqlens = ctx.saved_tensors
+        g = kda_short_conv_bwd(x, w, cu_seqlens, _grad(dy, x), bias=bias, initial_state=initial_state,
+                               dfinal_state=None if dlast is None else dlast.contiguous(), silu=ctx.silu, l2norm=ctx.l2norm)
+        return g["dx"], g["dw"], g["dbias"], g["dinitial_state"], None, None, None
+
+
+def short_conv(x, w, cu_seqlens, bias=None, initial_state=None, silu: bool = False, l2norm: bool = False):
+    """kda_short_conv_fwd as a differentiable function of x, w, bias and initial_state; its backward is
+    kda_short_conv_bwd.  Returns (y, final_state)."""
+    return _ShortConv.apply(x, w, bias, initial_state, cu_seqlens, bool(silu), bool(l2norm))
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, b, eps):
+        y, mean, rstd = kda_layer_norm_fwd(x, w, b, eps=eps)
+        ctx.save_for_backward(x, w, mean, rstd)
+        ctx.has_bias = b is not None
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, mean, rstd = ctx.saved_tensors
+        g = kda_layer_norm_bwd(x, w, mean, rstd, _grad(dy, x), has_bias=ctx.has_bias)
+        return g["dx"], g["dw"], g["dbias"], None
+
+
+def layer_norm(x, w, b=None, eps: float = 1e-5):
+    """kda_layer_norm_fwd as a differentiable function of x, w and b; its backward is kda_layer_norm_bwd."""
+    return _LayerNorm.apply(x, w, b, float(eps))
 
 
 def kda_launch_count() -> int:

@@ -9,7 +9,9 @@
 #include <cstdio>
 #include <mutex>
 #include <cstring>
+#include <initializer_list>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include "kda.h"
@@ -22,6 +24,10 @@
 #include "state_map.cuh"
 #include "backward.cuh"
 #include "backward_chunk.cuh"
+#include "selective_scan.cuh"
+#include "selective_scan_bwd.cuh"
+#include "conv_state.cuh"
+#include "layer_norm.cuh"
 
 namespace {
 
@@ -1221,4 +1227,653 @@ kda_status kda_chunk_bwd_chunkwise(const void *q, const void *k, const void *v, 
     if (d_k == 128 && d_v == 64) return launch_bwd_chunkwise<128, 64>(p, units, records, st);
     if (d_k == 64 && d_v == 128) return launch_bwd_chunkwise<64, 128>(p, units, records, st);
     return launch_bwd_chunkwise<64, 64>(p, units, records, st);
+}
+
+// ---- the selective scan, the convolution with its carried window, layer norm --------------------
+
+namespace {
+
+bool known_dtype(kda_dtype t) { return t == KDA_DTYPE_BF16 || t == KDA_DTYPE_F32; }
+
+size_t elem_size(kda_dtype t) { return t == KDA_DTYPE_BF16 ? 2 : 4; }
+
+// whether [a, a + na) and [b, b + nb) share bytes
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+// refuses an output that shares bytes with an input
+struct Span { const void *p; size_t bytes; };
+kda_status apart_check(const char *where, std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (const Span &o : outs)
+        for (const Span &i : ins)
+            if (overlap(o.p, o.bytes, i.p, i.bytes)) return fail(KDA_ERR_INVALID_ARG, std::string(where) + ": an output overlaps an input");
+    return KDA_OK;
+}
+
+kda_status launched(const char *where, int kernels = 1) {
+    g_launches.fetch_add(kernels, std::memory_order_relaxed);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, where);
+}
+
+constexpr int kScanMaxStates = 64;
+
+// lanes that hold the n states of a channel, four to a lane
+int scan_lanes(int n) {
+    int L = 1;
+    while (4 * L < n) L *= 2;
+    return L;
+}
+
+// f(integral_constant<int, L>) for the L of n states
+template <class F>
+kda_status with_lanes(int n, F f) {
+    switch (scan_lanes(n)) {
+        case 1: return f(std::integral_constant<int, 1>());
+        case 2: return f(std::integral_constant<int, 2>());
+        case 4: return f(std::integral_constant<int, 4>());
+        case 8: return f(std::integral_constant<int, 8>());
+        default: return f(std::integral_constant<int, 16>());
+    }
+}
+
+// f(integral_constant<bool, bf16>)
+template <class F>
+kda_status with_dtype(kda_dtype t, F f) {
+    return t == KDA_DTYPE_BF16 ? f(std::integral_constant<bool, true>()) : f(std::integral_constant<bool, false>());
+}
+
+int scan_channels(int n) { return kda::kScanThreads / scan_lanes(n); }             // of a block
+int scan_tile(int n) { const int L = scan_lanes(n); return L <= 4 ? 8 * L : 32; }  // tokens of a tile
+int scan_blocks_of_group(int D, int n, int G) { return (D / G + scan_channels(n) - 1) / scan_channels(n); }
+
+bool scan_sizes_ok(int64_t rows, int32_t seqs, int32_t D, int32_t n, int32_t G) {
+    return rows >= 0 && rows <= 0x7fffffffLL && seqs >= 0 && D > 0 && n > 0 && G > 0 && D % G == 0;
+}
+
+// Tokens of a segment of the prompt's scan; more than total_tokens where sequences are not cut (so that
+// an empty sequence at the very end has its record too).
+int64_t scan_segment_len(int64_t T, int32_t num_seqs, int32_t D, int32_t n, int32_t G) {
+    const int64_t blocks = (int64_t)G * scan_blocks_of_group(D, n, G), sms = device_sm_count();
+    if (blocks * num_seqs >= sms) return T + 1;
+    const int64_t want = std::max<int64_t>(1, 4 * sms / blocks);   // segments of the whole batch
+    const int64_t len = std::max<int64_t>(256, ((T + want - 1) / want + 63) / 64 * 64);
+    return len >= T ? T + 1 : len;
+}
+
+struct ScanSpace {   // floats of the workspace's parts
+    int64_t records;
+    size_t h, delta, h0, total;
+};
+
+ScanSpace scan_space(int64_t T, int32_t num_seqs, int32_t D, int32_t n, int32_t G) {
+    const int64_t len = scan_segment_len(T, num_seqs, D, n, G);
+    ScanSpace s{};
+    s.records = num_seqs;
+    if (len < T) {
+        s.records = T / len + num_seqs;
+        s.h = (size_t)s.records * D * n;
+        s.delta = ((size_t)s.records * D + 3) / 4 * 4;
+        s.h0 = (size_t)num_seqs * D * n;
+        s.h = (s.h + 3) / 4 * 4;
+    }
+    s.total = s.h + s.delta + s.h0;
+    return s;
+}
+
+int scan_elems(int n) { return scan_tile(n) * scan_channels(n) / kda::kScanThreads; }
+
+// the checks that the scan's entry points share; `where` names the entry point
+kda_status scan_check(const char *where, int64_t rows, int32_t seqs, int32_t D, int32_t n, int32_t G, kda_dtype dtype) {
+    const std::string w(where);
+    if (!scan_sizes_ok(rows, seqs, D, n, G))
+        return fail(KDA_ERR_INVALID_ARG, w + ": negative or too large size, or G does not divide D");
+    if (n > kScanMaxStates) return fail(KDA_ERR_UNSUPPORTED, w + ": more than 64 states per channel");
+    if (!known_dtype(dtype)) return fail(KDA_ERR_INVALID_ARG, w + ": dtype must be KDA_DTYPE_BF16 or KDA_DTYPE_F32");
+    return KDA_OK;
+}
+
+// Activations and states need their elements' alignment only; where all of a call's are 16-byte aligned, rows
+// that hold whole vectors are moved as vectors.
+kda_status aligned_check(const char *where, size_t elem, std::initializer_list<const void *> acts,
+                         std::initializer_list<const void *> floats, const void *workspace = nullptr) {
+    for (const void *p : acts)
+        if (p && !aligned(p, elem)) return fail(KDA_ERR_INVALID_ARG, std::string(where) + ": activation pointer not aligned to its type");
+    for (const void *p : floats)
+        if (p && !aligned(p, 4)) return fail(KDA_ERR_INVALID_ARG, std::string(where) + ": fp32 or cu_seqlens pointer not 4-byte aligned");
+    if (workspace && !aligned(workspace, 16)) return fail(KDA_ERR_INVALID_ARG, std::string(where) + ": workspace not 16-byte aligned");
+    return KDA_OK;
+}
+
+bool all_aligned(std::initializer_list<const void *> ptrs) {
+    for (const void *p : ptrs)
+        if (!aligned(p, 16)) return false;
+    return true;
+}
+
+kda_status space_check(const char *where, const void *workspace, size_t bytes, size_t need) {
+    if (need > 0 && (!workspace || bytes < need))
+        return fail(KDA_ERR_INVALID_ARG, std::string(where) + ": workspace missing or too small (need " + std::to_string(need) + " bytes)");
+    return KDA_OK;
+}
+
+}  // namespace
+
+size_t kda_selective_scan_fwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t D, int32_t n, int32_t G) {
+    if (!scan_sizes_ok(total_tokens, num_seqs, D, n, G) || n > kScanMaxStates || num_seqs == 0) return 0;
+    return scan_space(total_tokens, num_seqs, D, n, G).total * 4;
+}
+
+kda_status kda_selective_scan_fwd(const void *u, const void *dt, const float *A_log, const void *B, const void *C,
+                                  const float *skip, const void *z, const float *dt_bias, const int32_t *cu_seqlens,
+                                  int32_t num_seqs, int64_t total_tokens, int32_t D, int32_t n, int32_t G,
+                                  const float *initial_state, float *final_state, void *out, kda_dtype dtype,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    const char *where = "kda_selective_scan_fwd";
+    kda_status st = scan_check(where, total_tokens, num_seqs, D, n, G, dtype);
+    if (st != KDA_OK) return st;
+    if (num_seqs == 0) {
+        if (total_tokens != 0) return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_fwd: tokens without sequences");
+        return KDA_OK;
+    }
+    if (!A_log || !cu_seqlens || (total_tokens > 0 && (!u || !dt || !B || !C || !out)))
+        return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_fwd: NULL required pointer");
+    st = aligned_check(where, elem_size(dtype), {u, dt, B, C, z, out}, {A_log, skip, dt_bias, cu_seqlens, initial_state, final_state}, workspace);
+    if (st != KDA_OK) return st;
+    const size_t state_bytes = (size_t)num_seqs * D * n * 4;
+    if (initial_state != final_state && overlap(initial_state, state_bytes, final_state, state_bytes))
+        return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_fwd: final_state overlaps initial_state in part");
+    const size_t act = (size_t)total_tokens * D * elem_size(dtype), bc = (size_t)total_tokens * G * n * elem_size(dtype);
+    st = apart_check(where, {{out, act}}, {{u, act}, {dt, act}, {z, act}, {B, bc}, {C, bc}});
+    if (st != KDA_OK) return st;
+    const ScanSpace space = scan_space(total_tokens, num_seqs, D, n, G);
+    st = space_check(where, workspace, workspace_bytes, space.total * 4);
+    if (st != KDA_OK) return st;
+    kda::ScanParams p{};
+    p.u = u; p.dt = dt; p.z = z; p.B = B; p.C = C;
+    p.A_log = A_log; p.skip = skip; p.dt_bias = dt_bias;
+    p.cu = cu_seqlens;
+    p.h0 = initial_state;
+    p.hN = final_state;
+    p.out = out;
+    p.seg_h = static_cast<float *>(workspace);
+    p.seg_delta = p.seg_h + space.h;
+    p.seg_h0 = p.seg_delta + space.delta;
+    p.total_tokens = total_tokens;
+    p.num_seqs = num_seqs;
+    p.D = D; p.n = n; p.G = G;
+    p.cbg = scan_blocks_of_group(D, n, G);
+    p.seg_len = scan_segment_len(total_tokens, num_seqs, D, n, G);
+    p.vec = (D / G) % scan_elems(n) == 0 && all_aligned({u, dt, z, out});
+    p.vecn = n % 4 == 0 && all_aligned({B, C, initial_state, final_state});
+    const int64_t blocks = space.records * G * p.cbg;
+    if (blocks > 0x7fffffffLL) return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_fwd: too many sequences and channels");
+    const bool cut = space.total > 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return with_dtype(dtype, [&](auto bf16) {
+        return with_lanes(n, [&](auto lanes) {
+            constexpr bool kBf16 = decltype(bf16)::value;
+            constexpr int L = decltype(lanes)::value;
+            if (cut) kda::scan_fwd_kernel<kBf16, L, true><<<(unsigned)blocks, kda::kScanThreads, 0, s>>>(p);
+            kda::scan_fwd_kernel<kBf16, L, false><<<(unsigned)blocks, kda::kScanThreads, 0, s>>>(p);
+            return launched("selective_scan_fwd launch", cut ? 2 : 1);
+        });
+    });
+}
+
+kda_status kda_selective_scan_step(const void *u, const void *dt, const float *A_log, const void *B, const void *C,
+                                   const float *skip, const void *z, const float *dt_bias, float *state, void *out,
+                                   kda_dtype dtype, int32_t N, int32_t D, int32_t n, int32_t G, void *stream) {
+    const char *where = "kda_selective_scan_step";
+    kda_status st = scan_check(where, N, 0, D, n, G, dtype);
+    if (st != KDA_OK) return st;
+    if (N == 0) return KDA_OK;
+    if (!u || !dt || !A_log || !B || !C || !state || !out) return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_step: NULL required pointer");
+    st = aligned_check(where, elem_size(dtype), {u, dt, B, C, z, out}, {A_log, skip, dt_bias, state});
+    if (st != KDA_OK) return st;
+    const size_t act = (size_t)N * D * elem_size(dtype), bc = (size_t)N * G * n * elem_size(dtype);
+    st = apart_check(where, {{out, act}, {state, (size_t)N * D * n * 4}}, {{u, act}, {dt, act}, {z, act}, {B, bc}, {C, bc}});
+    if (st != KDA_OK) return st;
+    kda::ScanStepParams p{};
+    p.u = u; p.dt = dt; p.z = z; p.B = B; p.C = C;
+    p.A_log = A_log; p.skip = skip; p.dt_bias = dt_bias;
+    p.state = state;
+    p.out = out;
+    p.N = N; p.D = D; p.n = n; p.G = G;
+    p.vecn = n % 4 == 0 && all_aligned({B, C, state});
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return with_dtype(dtype, [&](auto bf16) {
+        return with_lanes(n, [&](auto lanes) {
+            constexpr bool kBf16 = decltype(bf16)::value;
+            constexpr int L = decltype(lanes)::value;
+            const int64_t bx = ((int64_t)D * L + kda::kScanStepThreads - 1) / kda::kScanStepThreads;
+            if (N >= 8) {
+                const dim3 grid((unsigned)bx, (unsigned)std::min<int64_t>((N + 3) / 4, 65535));
+                kda::scan_step_kernel<kBf16, L, 4><<<grid, kda::kScanStepThreads, 0, s>>>(p);
+            } else {
+                kda::scan_step_kernel<kBf16, L, 1><<<dim3((unsigned)bx, (unsigned)N), kda::kScanStepThreads, 0, s>>>(p);
+            }
+            return launched("selective_scan_step launch");
+        });
+    });
+}
+
+namespace {
+
+struct ScanBwdSpace {
+    int64_t records;
+    size_t state, chan, bc, total;   // floats
+};
+
+ScanBwdSpace scan_bwd_space(int64_t T, int32_t num_seqs, int32_t D, int32_t n, int32_t G) {
+    ScanBwdSpace s{};
+    s.records = T / (2 * scan_tile(n)) + num_seqs;
+    s.state = ((size_t)s.records * D * n + 3) / 4 * 4;
+    s.chan = ((size_t)s.records * D + 3) / 4 * 4;
+    s.bc = (size_t)G * scan_blocks_of_group(D, n, G) * T * 2 * n;
+    s.total = 2 * s.state + 3 * s.chan + s.bc;
+    return s;
+}
+
+}  // namespace
+
+size_t kda_selective_scan_bwd_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t D, int32_t n, int32_t G) {
+    if (!scan_sizes_ok(total_tokens, num_seqs, D, n, G) || n > kScanMaxStates || num_seqs == 0) return 0;
+    return scan_bwd_space(total_tokens, num_seqs, D, n, G).total * 4;
+}
+
+kda_status kda_selective_scan_bwd(const void *u, const void *dt, const float *A_log, const void *B, const void *C,
+                                  const float *skip, const void *z, const float *dt_bias, const int32_t *cu_seqlens,
+                                  int32_t num_seqs, int64_t total_tokens, int32_t D, int32_t n, int32_t G,
+                                  const float *initial_state, const void *dout, const float *dfinal_state, void *du,
+                                  void *ddt, float *dA_log, void *dB, void *dC, float *dskip, void *dz, float *ddt_bias,
+                                  float *dinitial_state, kda_dtype dtype, void *workspace, size_t workspace_bytes,
+                                  void *stream) {
+    const char *where = "kda_selective_scan_bwd";
+    kda_status st = scan_check(where, total_tokens, num_seqs, D, n, G, dtype);
+    if (st != KDA_OK) return st;
+    if (!dA_log) return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_bwd: NULL required pointer");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (num_seqs == 0) {
+        if (total_tokens != 0) return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_bwd: tokens without sequences");
+        cudaError_t e = cudaMemsetAsync(dA_log, 0, (size_t)D * n * 4, s);
+        if (e == cudaSuccess && dskip) e = cudaMemsetAsync(dskip, 0, (size_t)D * 4, s);
+        if (e == cudaSuccess && ddt_bias) e = cudaMemsetAsync(ddt_bias, 0, (size_t)D * 4, s);
+        return e == cudaSuccess ? KDA_OK : cuda_fail(e, "cudaMemsetAsync(selective_scan_bwd)");
+    }
+    if (!A_log || !cu_seqlens || (total_tokens > 0 && (!u || !dt || !B || !C || !dout || !du || !ddt || !dB || !dC)))
+        return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_bwd: NULL required pointer");
+    if (total_tokens > 0 && z && !dz) return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_bwd: z given without dz");
+    st = aligned_check(where, elem_size(dtype), {u, dt, B, C, z, dout, du, ddt, dB, dC, dz},
+                       {A_log, skip, dt_bias, cu_seqlens, initial_state, dfinal_state, dinitial_state, dA_log, dskip, ddt_bias}, workspace);
+    if (st != KDA_OK) return st;
+    const size_t act = (size_t)total_tokens * D * elem_size(dtype), bc = (size_t)total_tokens * G * n * elem_size(dtype);
+    st = apart_check(where, {{du, act}, {ddt, act}, {dz, act}, {dB, bc}, {dC, bc}},
+                     {{u, act}, {dt, act}, {z, act}, {dout, act}, {B, bc}, {C, bc}});
+    if (st != KDA_OK) return st;
+    const ScanBwdSpace space = scan_bwd_space(total_tokens, num_seqs, D, n, G);
+    st = space_check(where, workspace, workspace_bytes, space.total * 4);
+    if (st != KDA_OK) return st;
+    kda::ScanBwdParams p{};
+    p.u = u; p.dt = dt; p.z = z; p.B = B; p.C = C; p.dout = dout;
+    p.A_log = A_log; p.skip = skip; p.dt_bias = dt_bias;
+    p.cu = cu_seqlens;
+    p.h0 = initial_state;
+    p.dhN = dfinal_state;
+    p.du = du; p.ddt = ddt; p.dz = dz; p.dB = dB; p.dC = dC;
+    p.dA_log = dA_log; p.dskip = dskip; p.ddt_bias = ddt_bias; p.dh0 = dinitial_state;
+    p.H = static_cast<float *>(workspace);
+    p.R = p.H + space.state;
+    p.sum_delta = p.R + space.state;
+    p.pskip = p.sum_delta + space.chan;
+    p.pbias = p.pskip + space.chan;
+    p.pBC = p.pbias + space.chan;
+    p.total_tokens = total_tokens;
+    p.records = space.records;
+    p.num_seqs = num_seqs;
+    p.D = D; p.n = n; p.G = G;
+    p.cbg = scan_blocks_of_group(D, n, G);
+    p.vec = (D / G) % scan_elems(n) == 0 && all_aligned({u, dt, z, dout, du, ddt, dz});
+    p.vecn = n % 4 == 0 && all_aligned({B, C, initial_state, dfinal_state, dinitial_state});
+    const int64_t blocks = space.records * G * p.cbg, bc_blocks = (total_tokens * G * 2 * n + 255) / 256;
+    const int64_t w_blocks = ((int64_t)D * (n + 2) + 31) / 32;
+    if (blocks > 0x7fffffffLL || bc_blocks > 0x7fffffffLL || w_blocks > 0x7fffffffLL)
+        return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_bwd: too many tokens, sequences and channels");
+    return with_dtype(dtype, [&](auto bf16) {
+        return with_lanes(n, [&](auto lanes) {
+            constexpr bool kBf16 = decltype(bf16)::value;
+            constexpr int L = decltype(lanes)::value;
+            constexpr int smem = kda::ScanGradSmem<L>::kBytes;
+            const cudaError_t e = cudaFuncSetAttribute(kda::scan_bwd_grad_kernel<kBf16, L>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(selective_scan_bwd)");
+            kda::scan_bwd_chunk_kernel<kBf16, L><<<(unsigned)blocks, kda::kScanThreads, 0, s>>>(p);
+            const int64_t quads = (int64_t)D * L;
+            const dim3 chain((unsigned)((quads + kda::kChainThreads - 1) / kda::kChainThreads),
+                             (unsigned)std::min<int32_t>(num_seqs, 65535), 2);
+            kda::scan_bwd_chain_kernel<L><<<chain, kda::kChainThreads, 0, s>>>(p);
+            kda::scan_bwd_grad_kernel<kBf16, L><<<(unsigned)blocks, kda::kScanThreads, smem, s>>>(p);
+            if (bc_blocks > 0) kda::scan_bwd_bc_kernel<kBf16><<<(unsigned)bc_blocks, 256, 0, s>>>(p);
+            kda::scan_bwd_weights_kernel<<<(unsigned)w_blocks, dim3(32, kda::kColRows), 0, s>>>(p);
+            return launched("selective_scan_bwd launch", bc_blocks > 0 ? 5 : 4);
+        });
+    });
+}
+
+namespace {
+
+constexpr int kConvFwdElems16 = 8, kConvFwdElems32 = 4, kConvBwdElems = 4;
+
+// tokens of a run: enough blocks to fill the GPU several times, few enough that the W - 1 rows read
+// twice stay a small share
+int64_t conv_run_len(int64_t T, int64_t cblocks, int64_t lo, int64_t hi) {
+    const int64_t want = std::max<int64_t>(1, 8LL * device_sm_count() / cblocks);
+    return std::min(hi, std::max(lo, ((T + want - 1) / want + 7) / 8 * 8));
+}
+
+int64_t conv_channel_blocks(int64_t C, int E) { return (C + (int64_t)kda::kConvThreads * E - 1) / ((int64_t)kda::kConvThreads * E); }
+
+int64_t conv_bwd_run_len(int64_t T, int64_t C) { return conv_run_len(T, conv_channel_blocks(C, kConvBwdElems), 16, 128); }
+
+int64_t conv_bwd_runs(int64_t T, int64_t C) {
+    const int64_t len = conv_bwd_run_len(T, C);
+    return std::max<int64_t>(1, (T + len - 1) / len);
+}
+
+bool conv_sizes_ok(int64_t rows, int32_t seqs, int32_t H, int32_t d) {
+    return rows >= 0 && rows <= 0x7fffffffLL && seqs >= 0 && H > 0 && d > 0 && (int64_t)H * d <= 0x1000000LL;
+}
+
+kda_status conv_check(const char *where, int64_t rows, int32_t seqs, int32_t H, int32_t d, int32_t width, int32_t l2norm,
+                      kda_dtype dtype) {
+    const std::string w(where);
+    if (!conv_sizes_ok(rows, seqs, H, d)) return fail(KDA_ERR_INVALID_ARG, w + ": negative or too large size");
+    if (l2norm && !supported_dim(d)) return fail(KDA_ERR_UNSUPPORTED, w + ": with l2norm, d must be 64 or 128");
+    if (width < 1 || width > kda::kConvMaxWidth) return fail(KDA_ERR_INVALID_ARG, w + ": width must be in [1, 4]");
+    if (!known_dtype(dtype)) return fail(KDA_ERR_INVALID_ARG, w + ": dtype must be KDA_DTYPE_BF16 or KDA_DTYPE_F32");
+    return KDA_OK;
+}
+
+// f(integral_constant<int, W>)
+template <class F>
+kda_status with_width(int width, F f) {
+    switch (width) {
+        case 1: return f(std::integral_constant<int, 1>());
+        case 2: return f(std::integral_constant<int, 2>());
+        case 3: return f(std::integral_constant<int, 3>());
+        default: return f(std::integral_constant<int, 4>());
+    }
+}
+
+}  // namespace
+
+kda_status kda_short_conv_fwd(const void *x, const float *w, const float *bias, const int32_t *cu_seqlens, int32_t num_seqs,
+                              int64_t total_tokens, int32_t H, int32_t d, int32_t width, int32_t silu, int32_t l2norm,
+                              const void *initial_state, void *final_state, void *y, kda_dtype dtype, void *stream) {
+    const char *where = "kda_short_conv_fwd";
+    kda_status st = conv_check(where, total_tokens, num_seqs, H, d, width, l2norm, dtype);
+    if (st != KDA_OK) return st;
+    if (num_seqs == 0) {
+        if (total_tokens != 0) return fail(KDA_ERR_INVALID_ARG, "kda_short_conv_fwd: tokens without sequences");
+        return KDA_OK;
+    }
+    if (!w || !cu_seqlens || (total_tokens > 0 && (!x || !y))) return fail(KDA_ERR_INVALID_ARG, "kda_short_conv_fwd: NULL required pointer");
+    st = aligned_check(where, elem_size(dtype), {x, y, initial_state, final_state}, {w, bias, cu_seqlens});
+    if (st != KDA_OK) return st;
+    const int64_t C = (int64_t)H * d;
+    const size_t es = elem_size(dtype), rows_bytes = (size_t)total_tokens * C * es;
+    const size_t state_bytes = (size_t)num_seqs * (width - 1) * C * es;
+    st = apart_check(where, {{y, rows_bytes}}, {{x, rows_bytes}});
+    if (st != KDA_OK) return st;
+    if (initial_state != final_state && overlap(initial_state, state_bytes, final_state, state_bytes))
+        return fail(KDA_ERR_INVALID_ARG, "kda_short_conv_fwd: final_state overlaps initial_state in part");
+    kda::ConvStateParams p{};
+    p.x = x; p.w = w; p.bias = bias; p.cu = cu_seqlens;
+    p.h0 = initial_state;
+    p.y = y;
+    p.hN = final_state;
+    p.total_tokens = total_tokens;
+    p.num_seqs = num_seqs;
+    p.C = (int)C;
+    p.d = d;
+    p.silu = silu != 0;
+    p.l2norm = l2norm != 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return with_dtype(dtype, [&](auto bf16) {
+        return with_width(width, [&](auto taps) {
+            constexpr bool kBf16 = decltype(bf16)::value;
+            constexpr int W = decltype(taps)::value, E = kBf16 ? kConvFwdElems16 : kConvFwdElems32;
+            p.vec = C % E == 0 && all_aligned({x, y, initial_state, final_state});
+            const int64_t cblocks = conv_channel_blocks(C, E);
+            p.run_len = conv_run_len(total_tokens, cblocks, 8, 64);
+            p.runs = (total_tokens + p.run_len - 1) / p.run_len;
+            const int64_t states = final_state && W > 1 ? num_seqs : 0;
+            if (p.runs + states > 0x7fffffffLL || cblocks > 65535)
+                return fail(KDA_ERR_INVALID_ARG, "kda_short_conv_fwd: too many tokens or channels");
+            // the states' blocks beside the runs, or after them where they write what the runs read
+            const bool apart = states > 0 && final_state == initial_state && p.runs > 0;
+            const int64_t first = apart ? p.runs : p.runs + states;
+            if (first == 0) return KDA_OK;
+            kda::conv_state_fwd_kernel<kBf16, W, E><<<dim3((unsigned)first, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
+            if (apart) {
+                p.first_block = p.runs;
+                kda::conv_state_fwd_kernel<kBf16, W, E><<<dim3((unsigned)states, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
+            }
+            return launched("short_conv_fwd launch", apart ? 2 : 1);
+        });
+    });
+}
+
+kda_status kda_short_conv_step(const void *x, const float *w, const float *bias, void *state, int32_t N, int32_t H, int32_t d,
+                               int32_t width, int32_t silu, int32_t l2norm, void *y, kda_dtype dtype, void *stream) {
+    const char *where = "kda_short_conv_step";
+    kda_status st = conv_check(where, N, 0, H, d, width, l2norm, dtype);
+    if (st != KDA_OK) return st;
+    if (N == 0) return KDA_OK;
+    if (!x || !w || !y || (width > 1 && !state)) return fail(KDA_ERR_INVALID_ARG, "kda_short_conv_step: NULL required pointer");
+    st = aligned_check(where, elem_size(dtype), {x, y, state}, {w, bias});
+    if (st != KDA_OK) return st;
+    const int64_t C = (int64_t)H * d;
+    const size_t rows_bytes = (size_t)N * C * elem_size(dtype);
+    st = apart_check(where, {{y, rows_bytes}, {state, rows_bytes * (width - 1)}}, {{x, rows_bytes}});
+    if (st != KDA_OK) return st;
+    kda::ConvStateParams p{};
+    p.x = x; p.w = w; p.bias = bias;
+    p.h0 = state;
+    p.hN = state;
+    p.y = y;
+    p.num_seqs = N;
+    p.C = (int)C;
+    p.d = d;
+    p.silu = silu != 0;
+    p.l2norm = l2norm != 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return with_dtype(dtype, [&](auto bf16) {
+        return with_width(width, [&](auto taps) {
+            constexpr bool kBf16 = decltype(bf16)::value;
+            constexpr int W = decltype(taps)::value, E = kBf16 ? kConvFwdElems16 : kConvFwdElems32;
+            p.vec = C % E == 0 && all_aligned({x, y, state});
+            const int64_t cblocks = conv_channel_blocks(C, E);
+            if (cblocks > 65535) return fail(KDA_ERR_INVALID_ARG, "kda_short_conv_step: too many channels");
+            kda::conv_step_kernel<kBf16, W, E><<<dim3((unsigned)N, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
+            return launched("short_conv_step launch");
+        });
+    });
+}
+
+size_t kda_short_conv_bwd_workspace_size(int64_t total_tokens, int32_t H, int32_t d, int32_t width) {
+    if (!conv_sizes_ok(total_tokens, 0, H, d) || width < 1 || width > kda::kConvMaxWidth) return 0;
+    const int64_t C = (int64_t)H * d;
+    return (size_t)conv_bwd_runs(total_tokens, C) * (width + 1) * C * 4;
+}
+
+kda_status kda_short_conv_bwd(const void *x, const float *w, const float *bias, const int32_t *cu_seqlens, int32_t num_seqs,
+                              int64_t total_tokens, int32_t H, int32_t d, int32_t width, int32_t silu, int32_t l2norm,
+                              const void *initial_state, const void *dy, const void *dfinal_state, void *dx, float *dw,
+                              float *dbias, void *dinitial_state, kda_dtype dtype, void *workspace, size_t workspace_bytes,
+                              void *stream) {
+    const char *where = "kda_short_conv_bwd";
+    kda_status st = conv_check(where, total_tokens, num_seqs, H, d, width, l2norm, dtype);
+    if (st != KDA_OK) return st;
+    if (!w || !dw) return fail(KDA_ERR_INVALID_ARG, "kda_short_conv_bwd: NULL required pointer");
+    const int64_t C = (int64_t)H * d;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (num_seqs == 0) {
+        if (total_tokens != 0) return fail(KDA_ERR_INVALID_ARG, "kda_short_conv_bwd: tokens without sequences");
+        cudaError_t e = cudaMemsetAsync(dw, 0, (size_t)C * width * 4, s);
+        if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, (size_t)C * 4, s);
+        return e == cudaSuccess ? KDA_OK : cuda_fail(e, "cudaMemsetAsync(short_conv_bwd)");
+    }
+    if (!cu_seqlens || (total_tokens > 0 && (!x || !dy || !dx))) return fail(KDA_ERR_INVALID_ARG, "kda_short_conv_bwd: NULL required pointer");
+    st = aligned_check(where, elem_size(dtype), {x, dy, dx, initial_state, dfinal_state, dinitial_state}, {w, bias, cu_seqlens, dw, dbias},
+                       workspace);
+    if (st != KDA_OK) return st;
+    const size_t rows_bytes = (size_t)total_tokens * C * elem_size(dtype);
+    st = apart_check(where, {{dx, rows_bytes}}, {{x, rows_bytes}, {dy, rows_bytes}});
+    if (st != KDA_OK) return st;
+    st = space_check(where, workspace, workspace_bytes, kda_short_conv_bwd_workspace_size(total_tokens, H, d, width));
+    if (st != KDA_OK) return st;
+    kda::ConvStateParams p{};
+    p.x = x; p.dy = dy; p.w = w; p.bias = bias; p.cu = cu_seqlens;
+    p.h0 = initial_state;
+    p.dhN = dfinal_state;
+    p.y = dx;
+    p.dh0 = dinitial_state;
+    p.part = static_cast<float *>(workspace);
+    p.total_tokens = total_tokens;
+    p.run_len = conv_bwd_run_len(total_tokens, C);
+    p.runs = conv_bwd_runs(total_tokens, C);
+    p.num_seqs = num_seqs;
+    p.C = (int)C;
+    p.d = d;
+    p.vec = C % kConvBwdElems == 0 && all_aligned({x, dy, dx, initial_state, dfinal_state, dinitial_state});
+    p.silu = silu != 0;
+    p.l2norm = l2norm != 0;
+    const int64_t cblocks = conv_channel_blocks(C, kConvBwdElems);
+    if (cblocks > 65535) return fail(KDA_ERR_INVALID_ARG, "kda_short_conv_bwd: too many channels");
+    return with_dtype(dtype, [&](auto bf16) {
+        return with_width(width, [&](auto taps) {
+            constexpr bool kBf16 = decltype(bf16)::value;
+            constexpr int W = decltype(taps)::value;
+            kda::conv_state_bwd_kernel<kBf16, W, kConvBwdElems>
+                <<<dim3((unsigned)p.runs, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
+            const int64_t cols = (W + 1) * C;
+            kda::conv_weight_sum_kernel<<<(unsigned)((cols + 31) / 32), dim3(32, kda::kSumRows), 0, s>>>(p.part, p.runs, p.C, W, dw, dbias);
+            return launched("short_conv_bwd launch", 2);
+        });
+    });
+}
+
+namespace {
+
+constexpr int kNormMaxCols = 16384;
+
+// f(threads of a row, elements of a thread) for rows of d columns: a warp up to 256 columns, else a
+// block with as few threads as hold the row
+template <class F>
+kda_status with_row(int d, F f) {
+    using std::integral_constant;
+    if (d <= 256) return f(integral_constant<int, 32>(), integral_constant<int, 8>());
+    if (d <= 1024) return f(integral_constant<int, 128>(), integral_constant<int, 8>());
+    if (d <= 4096) return f(integral_constant<int, 512>(), integral_constant<int, 8>());
+    if (d <= 8192) return f(integral_constant<int, 512>(), integral_constant<int, 16>());
+    return f(integral_constant<int, 512>(), integral_constant<int, 32>());
+}
+
+// blocks of the backward pass: as many as run at once, each walking over rows
+int64_t norm_bwd_blocks(int64_t rows, int d) {
+    const int groups = d <= 256 ? 4 : 1;   // rows a block works on at once
+    const int64_t most = (int64_t)device_sm_count() * (d <= 1024 ? 6 : 2);
+    return std::max<int64_t>(1, std::min(most, (rows + groups - 1) / groups));
+}
+
+kda_status norm_check(const char *where, int64_t rows, int32_t d, kda_dtype dtype) {
+    const std::string w(where);
+    if (rows < 0 || d <= 0) return fail(KDA_ERR_INVALID_ARG, w + ": negative rows or d <= 0");
+    if (d > kNormMaxCols) return fail(KDA_ERR_UNSUPPORTED, w + ": more than 16384 columns");
+    if (!known_dtype(dtype)) return fail(KDA_ERR_INVALID_ARG, w + ": dtype must be KDA_DTYPE_BF16 or KDA_DTYPE_F32");
+    return KDA_OK;
+}
+
+}  // namespace
+
+kda_status kda_layer_norm_fwd(const void *x, const float *w, const float *b, int64_t rows, int32_t d, float eps, void *y,
+                              float *mean, float *rstd, kda_dtype dtype, void *stream) {
+    const char *where = "kda_layer_norm_fwd";
+    kda_status st = norm_check(where, rows, d, dtype);
+    if (st != KDA_OK) return st;
+    if (!(eps >= 0.f)) return fail(KDA_ERR_INVALID_ARG, "kda_layer_norm_fwd: eps must be >= 0");
+    if (rows == 0) return KDA_OK;
+    if (!x || !w || !y) return fail(KDA_ERR_INVALID_ARG, "kda_layer_norm_fwd: NULL required pointer");
+    st = aligned_check(where, elem_size(dtype), {x, y}, {w, b, mean, rstd});
+    if (st != KDA_OK) return st;
+    const size_t bytes = (size_t)rows * d * elem_size(dtype);
+    st = apart_check(where, {{y, bytes}}, {{x, bytes}});
+    if (st != KDA_OK) return st;
+    kda::NormParams p{};
+    p.x = x; p.w = w; p.b = b;
+    p.mean = mean; p.rstd = rstd;
+    p.y = y;
+    p.rows = rows;
+    p.d = d;
+    p.eps = eps;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return with_dtype(dtype, [&](auto bf16) {
+        return with_row(d, [&](auto row_threads, auto elems) {
+            constexpr bool kBf16 = decltype(bf16)::value;
+            constexpr int RT = decltype(row_threads)::value, EK = decltype(elems)::value;
+            using Block = kda::NormBlock<RT>;
+            p.vec = d % (kBf16 ? 8 : 4) == 0 && all_aligned({x, y});
+            const int64_t blocks = (rows + Block::kGroups - 1) / Block::kGroups;
+            if (blocks > 0x7fffffffLL) return fail(KDA_ERR_INVALID_ARG, "kda_layer_norm_fwd: too many rows");
+            kda::layer_norm_fwd_kernel<kBf16, RT, EK><<<(unsigned)blocks, Block::kThreads, 0, s>>>(p);
+            return launched("layer_norm_fwd launch");
+        });
+    });
+}
+
+size_t kda_layer_norm_bwd_workspace_size(int64_t rows, int32_t d) {
+    if (rows < 0 || d <= 0 || d > kNormMaxCols) return 0;
+    return (size_t)norm_bwd_blocks(rows, d) * (d <= 256 ? 4 : 1) * 2 * d * 4;
+}
+
+kda_status kda_layer_norm_bwd(const void *x, const float *w, const float *mean, const float *rstd, const void *dy,
+                              int64_t rows, int32_t d, void *dx, float *dw, float *db, kda_dtype dtype, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+    const char *where = "kda_layer_norm_bwd";
+    kda_status st = norm_check(where, rows, d, dtype);
+    if (st != KDA_OK) return st;
+    if (!w || !dw || (rows > 0 && (!x || !mean || !rstd || !dy || !dx)))
+        return fail(KDA_ERR_INVALID_ARG, "kda_layer_norm_bwd: NULL required pointer");
+    st = aligned_check(where, elem_size(dtype), {x, dy, dx}, {w, mean, rstd, dw, db}, workspace);
+    if (st != KDA_OK) return st;
+    const size_t bytes = (size_t)rows * d * elem_size(dtype);
+    st = apart_check(where, {{dx, bytes}}, {{x, bytes}, {dy, bytes}});
+    if (st != KDA_OK) return st;
+    st = space_check(where, workspace, workspace_bytes, kda_layer_norm_bwd_workspace_size(rows, d));
+    if (st != KDA_OK) return st;
+    kda::NormParams p{};
+    p.x = x; p.dy = dy; p.w = w;
+    p.mean = const_cast<float *>(mean);
+    p.rstd = const_cast<float *>(rstd);
+    p.y = dx;
+    p.part = static_cast<float *>(workspace);
+    p.rows = rows;
+    p.d = d;
+    const int64_t blocks = norm_bwd_blocks(rows, d);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return with_dtype(dtype, [&](auto bf16) {
+        return with_row(d, [&](auto row_threads, auto elems) {
+            constexpr bool kBf16 = decltype(bf16)::value;
+            constexpr int RT = decltype(row_threads)::value, EK = decltype(elems)::value;
+            using Block = kda::NormBlock<RT>;
+            p.vec = d % (kBf16 ? 8 : 4) == 0 && all_aligned({x, dy, dx});
+            kda::layer_norm_bwd_kernel<kBf16, RT, EK><<<(unsigned)blocks, Block::kThreads, 0, s>>>(p);
+            kda::norm_weight_sum_kernel<<<(unsigned)((2 * d + 31) / 32), dim3(32, kda::kSumRows), 0, s>>>(
+                p.part, blocks * Block::kGroups, d, dw, db);
+            return launched("layer_norm_bwd launch", 2);
+        });
+    });
 }
