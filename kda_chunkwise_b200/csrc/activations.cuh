@@ -1,7 +1,6 @@
 // Activations of either storage type (bf16 or fp32), read as vectors where every row starts on a
-// vector boundary and element by element elsewhere.  A piece of N consecutive elements is held as
-// raw words between the load and its use, so that a prefetched piece costs no conversion (and no
-// wait) at the load.
+// vector boundary and element by element elsewhere.  A piece of N elements is held as raw words between
+// the load and its use, so that a prefetched piece costs no conversion (and no wait) at the load.
 #pragma once
 
 #include "common.cuh"
@@ -18,91 +17,90 @@ struct Piece {
     uint32_t w[N];   // vector loads of bf16 fill the lower half; element loads take a word each
 };
 
-// A load through the read-only path, or (RO false) one that may be followed by a store to the same place.
-template <bool RO, class V>
-__device__ __forceinline__ V load_value(const V *p) {
-    if constexpr (RO) return __ldg(p);
-    else return *p;
+// Loads of 2, 4, 8 or 16 bytes where `on`, else the words stay as they are.  Written as predicated
+// instructions: a branch around a load would make the compiler wait for it at the join, and a prefetch
+// would be none.  RO: through the read-only path (not for what the kernel also writes).
+template <int BYTES, bool RO>
+__device__ __forceinline__ void load_if(const void *p, bool on, uint32_t *w) {
+    const int o = on;
+    if constexpr (BYTES == 2 && RO)
+        asm volatile("{.reg .pred q; setp.ne.s32 q, %2, 0; @q ld.global.nc.u16 %0, [%1];}" : "+r"(w[0]) : "l"(p), "r"(o));
+    else if constexpr (BYTES == 2)
+        asm volatile("{.reg .pred q; setp.ne.s32 q, %2, 0; @q ld.global.u16 %0, [%1];}" : "+r"(w[0]) : "l"(p), "r"(o) : "memory");
+    else if constexpr (BYTES == 4 && RO)
+        asm volatile("{.reg .pred q; setp.ne.s32 q, %2, 0; @q ld.global.nc.b32 %0, [%1];}" : "+r"(w[0]) : "l"(p), "r"(o));
+    else if constexpr (BYTES == 4)
+        asm volatile("{.reg .pred q; setp.ne.s32 q, %2, 0; @q ld.global.b32 %0, [%1];}" : "+r"(w[0]) : "l"(p), "r"(o) : "memory");
+    else if constexpr (BYTES == 8 && RO)
+        asm volatile("{.reg .pred q; setp.ne.s32 q, %3, 0; @q ld.global.nc.v2.b32 {%0, %1}, [%2];}"
+                     : "+r"(w[0]), "+r"(w[1]) : "l"(p), "r"(o));
+    else if constexpr (BYTES == 8)
+        asm volatile("{.reg .pred q; setp.ne.s32 q, %3, 0; @q ld.global.v2.b32 {%0, %1}, [%2];}"
+                     : "+r"(w[0]), "+r"(w[1]) : "l"(p), "r"(o) : "memory");
+    else if constexpr (RO)
+        asm volatile("{.reg .pred q; setp.ne.s32 q, %5, 0; @q ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];}"
+                     : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]) : "l"(p), "r"(o));
+    else
+        asm volatile("{.reg .pred q; setp.ne.s32 q, %5, 0; @q ld.global.v4.b32 {%0, %1, %2, %3}, [%4];}"
+                     : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]) : "l"(p), "r"(o) : "memory");
 }
 
-// N elements from element `off` on; only the first `valid` are read, the others are zero.  `vec`:
-// off is a multiple of N, N elements are 4 bytes or more, and valid is 0 or N.
-template <bool BF16, int N, bool RO = true>
-__device__ __forceinline__ void load_piece(const void *p, int64_t off, int valid, bool vec, Piece<BF16, N> &r) {
-    constexpr int kBytes = N * (BF16 ? 2 : 4);
-    if constexpr (kBytes >= 4) {
-        if (vec) {
-            constexpr int kOne = kBytes > 16 ? 16 : kBytes;
-            using V = typename VecOf<kOne>::type;
-            const char *src = static_cast<const char *>(p) + off * (BF16 ? 2 : 4);
+// N elements from element `off` on, `step` apart; only the first `valid` are read, the others are zero.
+// VEC: as vectors (step is 1, off is a multiple of N, valid is 0 or N).
+template <bool BF16, int N, bool VEC, bool RO = true>
+__device__ __forceinline__ void load_piece(const void *p, int64_t off, int valid, Piece<BF16, N> &r, int step = 1) {
+    constexpr int kElem = BF16 ? 2 : 4, kBytes = N * kElem;
+    const char *src = static_cast<const char *>(p) + off * kElem;
 #pragma unroll
-            for (int i = 0; i < kBytes / kOne; ++i) {
-                union { V v; uint32_t w[kOne / 4]; } x;
-                if (valid > 0) x.v = load_value<RO>(reinterpret_cast<const V *>(src) + i);
-                else
+    for (int i = 0; i < N; ++i) r.w[i] = 0u;
+    if constexpr (VEC) {
+        constexpr int kOne = kBytes > 16 ? 16 : kBytes;
 #pragma unroll
-                    for (int k = 0; k < kOne / 4; ++k) x.w[k] = 0u;
+        for (int i = 0; i < kBytes / kOne; ++i) load_if<kOne, RO>(src + i * kOne, valid > 0, r.w + i * (kOne / 4));
+    } else {
 #pragma unroll
-                for (int k = 0; k < kOne / 4; ++k) r.w[i * (kOne / 4) + k] = x.w[k];
-            }
-            return;
-        }
+        for (int i = 0; i < N; ++i) load_if<kElem, RO>(src + (int64_t)i * step * kElem, i < valid, r.w + i);
     }
+}
+
+template <bool BF16, int N, bool VEC>
+__device__ __forceinline__ void piece_to_f32(const Piece<BF16, N> &r, float (&v)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        if constexpr (BF16) r.w[i] = i < valid ? (uint32_t)load_value<RO>(static_cast<const uint16_t *>(p) + off + i) : 0u;
-        else r.w[i] = i < valid ? load_value<RO>(static_cast<const uint32_t *>(p) + off + i) : 0u;
+        if constexpr (!BF16) v[i] = __uint_as_float(r.w[i]);
+        else if constexpr (VEC) v[i] = __uint_as_float((i & 1) ? (r.w[i / 2] & 0xFFFF0000u) : (r.w[i / 2] << 16));
+        else v[i] = __uint_as_float(r.w[i] << 16);
     }
 }
 
-template <bool BF16, int N>
-__device__ __forceinline__ void piece_to_f32(const Piece<BF16, N> &r, bool vec, float (&v)[N]) {
-    if constexpr (!BF16) {
+__device__ __forceinline__ uint32_t pack2_bf16(float x, float y) {
+    return (uint32_t)f32_to_bf16(x) | ((uint32_t)f32_to_bf16(y) << 16);
+}
+
+// Rounds once to the storage type and stores the first `valid` of N elements (as load_piece).
+template <bool BF16, int N, bool VEC>
+__device__ __forceinline__ void store_piece(void *p, int64_t off, int valid, const float (&v)[N], int step = 1) {
+    if constexpr (VEC) {
+        if (valid <= 0) return;
+        constexpr int kBytes = N * (BF16 ? 2 : 4), kOne = kBytes > 16 ? 16 : kBytes;
+        using V = typename VecOf<kOne>::type;
+        char *dst = static_cast<char *>(p) + off * (BF16 ? 2 : 4);
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r.w[i]);
+        for (int i = 0; i < kBytes / kOne; ++i) {
+            union { V v; uint32_t w[kOne / 4]; } x;
+#pragma unroll
+            for (int k = 0; k < kOne / 4; ++k) {
+                const int e = i * (kOne / 4) + k;
+                if constexpr (BF16) x.w[k] = pack2_bf16(v[2 * e], v[2 * e + 1]);
+                else x.w[k] = __float_as_uint(v[e]);
+            }
+            reinterpret_cast<V *>(dst)[i] = x.v;
+        }
     } else {
-        if constexpr (N >= 2) {
-            if (vec) {
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    v[i] = __uint_as_float((i & 1) ? (r.w[i / 2] & 0xFFFF0000u) : (r.w[i / 2] << 16));
-                return;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r.w[i] << 16);
+        for (int i = 0; i < N; ++i)
+            if (i < valid) store_out(p, off + (int64_t)i * step, !BF16, v[i]);
     }
-}
-
-// Rounds once to the storage type and stores the first `valid` of N elements.
-template <bool BF16, int N>
-__device__ __forceinline__ void store_piece(void *p, int64_t off, int valid, bool vec, const float (&v)[N]) {
-    constexpr int kBytes = N * (BF16 ? 2 : 4);
-    if constexpr (kBytes >= 4) {
-        if (vec) {
-            if (valid <= 0) return;
-            constexpr int kOne = kBytes > 16 ? 16 : kBytes;
-            using V = typename VecOf<kOne>::type;
-            char *dst = static_cast<char *>(p) + off * (BF16 ? 2 : 4);
-#pragma unroll
-            for (int i = 0; i < kBytes / kOne; ++i) {
-                union { V v; uint32_t w[kOne / 4]; } x;
-#pragma unroll
-                for (int k = 0; k < kOne / 4; ++k) {
-                    const int e = i * (kOne / 4) + k;
-                    if constexpr (BF16)
-                        x.w[k] = (uint32_t)f32_to_bf16(v[2 * e]) | ((uint32_t)f32_to_bf16(v[2 * e + 1]) << 16);
-                    else
-                        x.w[k] = __float_as_uint(v[e]);
-                }
-                reinterpret_cast<V *>(dst)[i] = x.v;
-            }
-            return;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (i < valid) store_out(p, off + i, !BF16, v[i]);
 }
 
 template <bool BF16>
@@ -122,28 +120,49 @@ __device__ __forceinline__ void check_seqlens(const int32_t *cu, int num_seqs, i
     if (!ok) atomicOr(&g_kda_error_word, kErrBadSeqlens);
 }
 
-// log(1 + exp(x)), to fp32 precision at both ends
+// log(1 + exp(x)), to a few units in the last place at both ends: max(x, 0) + log1p(e), e = exp(-|x|), with
+// log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, and atanh(s) / s by the polynomial of degree four in s^2 of least
+// relative error on [0, 1/9] (Remez exchange: 4e-9).
 __device__ __forceinline__ float softplus(float x) {
-    const float e = log1pf(expf(-fabsf(x)));
-    return x > 0.f ? x + e : e;
+    const float e = ex2_approx(-1.4426950408889634f * fabsf(x));
+    const float s = e * rcp_approx(2.f + e), q = s * s;
+    float r = fmaf(q, 0.1408916711807251f, 0.13980300724506378f);
+    r = fmaf(r, q, 0.20012454688549042f);
+    r = fmaf(r, q, 0.3333315849304199f);
+    r = fmaf(r, q, 1.f);
+    return fmaf(2.f * s, r, fmaxf(x, 0.f));   // (a NaN passes through s)
 }
 
-// Sum over the L lanes that hold one channel, for L values at once: lane l (of L) is left with the
-// total of v[l].  Each step sends half of what is left to the partner lane, so L values take L - 1
-// shuffles instead of L log2(L).
-template <int L>
-__device__ __forceinline__ float transposed_sum(float (&v)[L], int lane) {
+// 1 - exp(-x) for x >= 0, to a few units in the last place: the series below 1/4 (the first term left out is
+// below 5e-8 of the sum), the difference above.
+__device__ __forceinline__ float one_minus_exp_neg(float x) {
+    float r = fmaf(x, -1.f / 720.f, 1.f / 120.f);
+    r = fmaf(r, x, -1.f / 24.f);
+    r = fmaf(r, x, 1.f / 6.f);
+    r = fmaf(r, x, -0.5f);
+    r = fmaf(r, x, 1.f);
+    return x < 0.25f ? x * r : 1.f - ex2_approx(-1.4426950408889634f * x);
+}
+
+// Sum over LANES lanes (STRIDE apart, this one the idx-th) for V values at once: lane idx is left
+// with the totals of v[idx V / LANES] .. in v[0] ..  Each step sends half of what is left to the
+// partner lane, so V values take under V shuffles instead of V log2(LANES).
+template <int V, int LANES, int STRIDE>
+__device__ __forceinline__ void transposed_sums(float (&v)[V], int idx) {
+    static_assert(V % LANES == 0, "a whole number of values a lane");
+    int half = V / 2;
 #pragma unroll
-    for (int w = L / 2; w > 0; w >>= 1) {
-        const bool upper = lane & w;
+    for (int w = LANES / 2; w > 0; w >>= 1) {
+        const bool upper = idx & w;
 #pragma unroll
-        for (int i = 0; i < w; ++i) {
-            const float keep = upper ? v[i + w] : v[i];
-            const float give = upper ? v[i] : v[i + w];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+        for (int i = 0; i < V / 2; ++i) {
+            if (i >= half) break;
+            const float keep = upper ? v[i + half] : v[i];
+            const float give = upper ? v[i] : v[i + half];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, w * STRIDE);
         }
+        half >>= 1;
     }
-    return v[0];
 }
 
 }  // namespace kda

@@ -28,37 +28,26 @@ struct ConvStateParams {
     float *part;                        // [runs, W + 1, C] the run's share of dw and dbias (backward)
     int64_t total_tokens, run_len, runs, first_block;
     int num_seqs, C, d;
-    bool vec, silu, l2norm;
+    bool silu, l2norm;
 };
 
-// The channels of a thread: c0 + i step.
-template <bool BF16, int E>
+// The channels of a thread: c0 + i step (VEC: consecutive, moved as vectors).
+template <bool BF16, int E, bool VEC>
 struct ChannelGroup {
     int64_t c0;
-    int step;
+    static constexpr int step = VEC ? 1 : kConvThreads;
     int count;   // how many of the E are channels
-    bool vec;
 
-    __device__ __forceinline__ ChannelGroup(int64_t block, int C, bool v) : vec(v) {
-        c0 = block * kConvThreads * E + (v ? (int64_t)threadIdx.x * E : threadIdx.x);
-        step = v ? 1 : kConvThreads;
-        int64_t n = c0 < C ? (C - c0 + step - 1) / step : 0;
+    __device__ __forceinline__ ChannelGroup(int64_t block, int C) {
+        c0 = block * kConvThreads * E + (VEC ? (int64_t)threadIdx.x * E : threadIdx.x);
+        const int64_t n = c0 < C ? (C - c0 + step - 1) / step : 0;
         count = static_cast<int>(n > E ? E : n);
     }
     template <bool RO = true>
     __device__ __forceinline__ void load(const void *p, int64_t row, bool on, Piece<BF16, E> &r) const {
-        const int n = on ? count : 0;
-        if (vec) {
-            load_piece<BF16, E, RO>(p, row + c0, n, true, r);
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if constexpr (BF16) r.w[i] = i < n ? (uint32_t)load_value<RO>(static_cast<const uint16_t *>(p) + row + c0 + i * step) : 0u;
-            else r.w[i] = i < n ? load_value<RO>(static_cast<const uint32_t *>(p) + row + c0 + i * step) : 0u;
-        }
+        load_piece<BF16, E, VEC, RO>(p, row + c0, on ? count : 0, r, step);
     }
-    __device__ __forceinline__ void get(const Piece<BF16, E> &r, float (&v)[E]) const { piece_to_f32<BF16, E>(r, vec, v); }
+    __device__ __forceinline__ void get(const Piece<BF16, E> &r, float (&v)[E]) const { piece_to_f32<BF16, E, VEC>(r, v); }
     template <bool RO = true>
     __device__ __forceinline__ void load_f32(const void *p, int64_t row, bool on, float (&v)[E]) const {
         Piece<BF16, E> r;
@@ -66,13 +55,7 @@ struct ChannelGroup {
         get(r, v);
     }
     __device__ __forceinline__ void store(void *p, int64_t row, const float (&v)[E]) const {
-        if (vec) {
-            store_piece<BF16, E>(p, row + c0, count, true, v);
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (i < count) store_out(p, row + c0 + i * step, !BF16, v[i]);
+        store_piece<BF16, E, VEC>(p, row + c0, count, v, step);
     }
 };
 
@@ -127,8 +110,8 @@ __device__ __forceinline__ void slide(float (&xw)[W > 1 ? W - 1 : 1][E], const f
 }
 
 // The window before token t of a sequence starting at s0: inputs, or rows of its carried state.
-template <bool BF16, int W, int E>
-__device__ __forceinline__ void load_window(const ConvStateParams &p, const ChannelGroup<BF16, E> &cg, int64_t t, int64_t s0,
+template <int W, int E, class Group>
+__device__ __forceinline__ void load_window(const ConvStateParams &p, const Group &cg, int64_t t, int64_t s0,
                                             int64_t seq, float (&xw)[W > 1 ? W - 1 : 1][E]) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
@@ -145,9 +128,9 @@ constexpr int kConvRows = 8;   // rows in flight per thread, forward
 
 // grid: x = runs of run_len tokens, then one block per sequence for the final states; y = blocks of
 // channels.  With hN = h0 the two are separate launches (first_block skips the runs).
-template <bool BF16, int W, int E>
+template <bool BF16, int W, int E, bool VEC>
 __global__ void __launch_bounds__(kConvThreads) conv_state_fwd_kernel(const ConvStateParams p) {
-    const ChannelGroup<BF16, E> cg(blockIdx.y, p.C, p.vec);
+    const ChannelGroup<BF16, E, VEC> cg(blockIdx.y, p.C);
     const int64_t bx = p.first_block + blockIdx.x;
     if (bx == 0 && blockIdx.y == 0) check_seqlens(p.cu, p.num_seqs, p.total_tokens);
     float xw[W > 1 ? W - 1 : 1][E];
@@ -155,7 +138,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_state_fwd_kernel(const Conv
         const int64_t seq = bx - p.runs;
         int64_t s0, s1;
         seq_span(p.cu, (int)seq, p.num_seqs, p.total_tokens, s0, s1);
-        load_window<BF16, W, E>(p, cg, s1, s0, seq, xw);
+        load_window<W, E>(p, cg, s1, s0, seq, xw);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) cg.store(p.hN, (seq * (W - 1) + j) * p.C, xw[j]);
         return;
@@ -165,7 +148,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_state_fwd_kernel(const Conv
     const int64_t r0 = bx * p.run_len, r1 = min64(r0 + p.run_len, p.total_tokens);
     int64_t seq = seq_of(p.cu, p.num_seqs, r0), s0, s1;
     seq_span(p.cu, (int)seq, p.num_seqs, p.total_tokens, s0, s1);
-    load_window<BF16, W, E>(p, cg, r0, s0, seq, xw);
+    load_window<W, E>(p, cg, r0, s0, seq, xw);
     for (int64_t t0 = r0; t0 < r1; t0 += kConvRows) {
         Piece<BF16, E> rx[kConvRows];
 #pragma unroll
@@ -177,7 +160,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_state_fwd_kernel(const Conv
             if (t >= s1 && seq + 1 < p.num_seqs) {   // the next sequence that has tokens starts here
                 do seq_span(p.cu, (int)++seq, p.num_seqs, p.total_tokens, s0, s1);
                 while (t >= s1 && seq + 1 < p.num_seqs);
-                load_window<BF16, W, E>(p, cg, t, t, seq, xw);
+                load_window<W, E>(p, cg, t, t, seq, xw);
             }
             float x[E], y[E];
             cg.get(rx[k], x);
@@ -189,9 +172,9 @@ __global__ void __launch_bounds__(kConvThreads) conv_state_fwd_kernel(const Conv
 }
 
 // One token of num_seqs sequences; the state (hN) in place.
-template <bool BF16, int W, int E>
+template <bool BF16, int W, int E, bool VEC>
 __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(const ConvStateParams p) {
-    const ChannelGroup<BF16, E> cg(blockIdx.y, p.C, p.vec);
+    const ChannelGroup<BF16, E, VEC> cg(blockIdx.y, p.C);
     float w[W][E], bias[E];
     load_taps<W, E>(p, cg, w, bias);
     for (int64_t r = blockIdx.x; r < p.num_seqs; r += gridDim.x) {
@@ -214,9 +197,9 @@ constexpr int kConvBackRows = 4;   // rows of x and dy in flight per thread, bac
 //   dx_u = sum_{i < W} w[W-1-i] q_{u+i}    (tokens of the same sequence only).
 // A run reads W - 1 tokens past its end to complete its last inputs.  Positions before a sequence's
 // first token are the rows of its carried state.
-template <bool BF16, int W, int E>
+template <bool BF16, int W, int E, bool VEC>
 __global__ void __launch_bounds__(kConvThreads) conv_state_bwd_kernel(const ConvStateParams p) {
-    const ChannelGroup<BF16, E> cg(blockIdx.y, p.C, p.vec);
+    const ChannelGroup<BF16, E, VEC> cg(blockIdx.y, p.C);
     if (blockIdx.x == 0 && blockIdx.y == 0) check_seqlens(p.cu, p.num_seqs, p.total_tokens);
     float w[W][E], bias[E], dw[W][E], db[E];
     load_taps<W, E>(p, cg, w, bias);
@@ -243,7 +226,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_state_bwd_kernel(const Conv
         const int64_t p0 = s0 > r0 ? s0 : r0, p1 = min64(s1, r1);   // this run's tokens of the sequence
         if (p0 > p1 || (p0 == p1 && s0 != s1)) continue;
         float xw[W > 1 ? W - 1 : 1][E], qw[W > 1 ? W - 1 : 1][E];   // inputs and gradients of the last W - 1 tokens
-        load_window<BF16, W, E>(p, cg, p0, s0, seq, xw);
+        load_window<W, E>(p, cg, p0, s0, seq, xw);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
 #pragma unroll

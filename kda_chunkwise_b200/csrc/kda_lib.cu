@@ -1285,9 +1285,10 @@ kda_status with_dtype(kda_dtype t, F f) {
     return t == KDA_DTYPE_BF16 ? f(std::integral_constant<bool, true>()) : f(std::integral_constant<bool, false>());
 }
 
-int scan_channels(int n) { return kda::kScanThreads / scan_lanes(n); }             // of a block
-int scan_tile(int n) { const int L = scan_lanes(n); return L <= 4 ? 8 * L : 32; }  // tokens of a tile
-int scan_blocks_of_group(int D, int n, int G) { return (D / G + scan_channels(n) - 1) / scan_channels(n); }
+// channels of a block of scanning threads that take KC channels each, and such blocks of a group
+int scan_channels(int n, int KC) { return KC * (kda::kScanThreads / scan_lanes(n)); }
+int scan_blocks_of_group(int D, int n, int G, int KC) { return (D / G + scan_channels(n, KC) - 1) / scan_channels(n, KC); }
+int scan_bwd_chunk(int n) { const int L = scan_lanes(n); return L >= 4 ? 64 : 16 * L; }   // ScanBwdTile::kTC
 
 bool scan_sizes_ok(int64_t rows, int32_t seqs, int32_t D, int32_t n, int32_t G) {
     return rows >= 0 && rows <= 0x7fffffffLL && seqs >= 0 && D > 0 && n > 0 && G > 0 && D % G == 0;
@@ -1296,9 +1297,9 @@ bool scan_sizes_ok(int64_t rows, int32_t seqs, int32_t D, int32_t n, int32_t G) 
 // Tokens of a segment of the prompt's scan; more than total_tokens where sequences are not cut (so that
 // an empty sequence at the very end has its record too).
 int64_t scan_segment_len(int64_t T, int32_t num_seqs, int32_t D, int32_t n, int32_t G) {
-    const int64_t blocks = (int64_t)G * scan_blocks_of_group(D, n, G), sms = device_sm_count();
-    if (blocks * num_seqs >= sms) return T + 1;
-    const int64_t want = std::max<int64_t>(1, 4 * sms / blocks);   // segments of the whole batch
+    const int64_t blocks = (int64_t)G * scan_blocks_of_group(D, n, G, 1), sms = device_sm_count();
+    if (2 * blocks * num_seqs >= sms) return T + 1;
+    const int64_t want = std::max<int64_t>(1, 2 * sms / blocks);   // segments of the whole batch
     const int64_t len = std::max<int64_t>(256, ((T + want - 1) / want + 63) / 64 * 64);
     return len >= T ? T + 1 : len;
 }
@@ -1323,7 +1324,17 @@ ScanSpace scan_space(int64_t T, int32_t num_seqs, int32_t D, int32_t n, int32_t 
     return s;
 }
 
-int scan_elems(int n) { return scan_tile(n) * scan_channels(n) / kda::kScanThreads; }
+template <bool BF16, int L>
+kda_status launch_scan_fwd(const kda::ScanParams &p, int64_t blocks, bool cut, cudaStream_t s) {
+    constexpr int smem = kda::ScanSmem<BF16, L>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(kda::scan_fwd_kernel<BF16, L, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && cut)
+        e = cudaFuncSetAttribute(kda::scan_fwd_kernel<BF16, L, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(selective_scan_fwd)");
+    if (cut) kda::scan_fwd_kernel<BF16, L, true><<<(unsigned)blocks, kda::kScanThreads + kda::kStageThreads, smem, s>>>(p);
+    kda::scan_fwd_kernel<BF16, L, false><<<(unsigned)blocks, kda::kScanThreads + kda::kStageThreads, smem, s>>>(p);
+    return launched("selective_scan_fwd launch", cut ? 2 : 1);
+}
 
 // the checks that the scan's entry points share; `where` names the entry point
 kda_status scan_check(const char *where, int64_t rows, int32_t seqs, int32_t D, int32_t n, int32_t G, kda_dtype dtype) {
@@ -1404,10 +1415,10 @@ kda_status kda_selective_scan_fwd(const void *u, const void *dt, const float *A_
     p.total_tokens = total_tokens;
     p.num_seqs = num_seqs;
     p.D = D; p.n = n; p.G = G;
-    p.cbg = scan_blocks_of_group(D, n, G);
     p.seg_len = scan_segment_len(total_tokens, num_seqs, D, n, G);
-    p.vec = (D / G) % scan_elems(n) == 0 && all_aligned({u, dt, z, out});
+    p.vec = (D / G) % 4 == 0 && all_aligned({u, dt, z, out});
     p.vecn = n % 4 == 0 && all_aligned({B, C, initial_state, final_state});
+    p.cbg = scan_blocks_of_group(D, n, G, 1);
     const int64_t blocks = space.records * G * p.cbg;
     if (blocks > 0x7fffffffLL) return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_fwd: too many sequences and channels");
     const bool cut = space.total > 0;
@@ -1416,9 +1427,7 @@ kda_status kda_selective_scan_fwd(const void *u, const void *dt, const float *A_
         return with_lanes(n, [&](auto lanes) {
             constexpr bool kBf16 = decltype(bf16)::value;
             constexpr int L = decltype(lanes)::value;
-            if (cut) kda::scan_fwd_kernel<kBf16, L, true><<<(unsigned)blocks, kda::kScanThreads, 0, s>>>(p);
-            kda::scan_fwd_kernel<kBf16, L, false><<<(unsigned)blocks, kda::kScanThreads, 0, s>>>(p);
-            return launched("selective_scan_fwd launch", cut ? 2 : 1);
+            return launch_scan_fwd<kBf16, L>(p, blocks, cut, s);
         });
     });
 }
@@ -1469,10 +1478,10 @@ struct ScanBwdSpace {
 
 ScanBwdSpace scan_bwd_space(int64_t T, int32_t num_seqs, int32_t D, int32_t n, int32_t G) {
     ScanBwdSpace s{};
-    s.records = T / (2 * scan_tile(n)) + num_seqs;
+    s.records = T / scan_bwd_chunk(n) + num_seqs;
     s.state = ((size_t)s.records * D * n + 3) / 4 * 4;
     s.chan = ((size_t)s.records * D + 3) / 4 * 4;
-    s.bc = (size_t)G * scan_blocks_of_group(D, n, G) * T * 2 * n;
+    s.bc = (size_t)G * scan_blocks_of_group(D, n, G, kda::kBackKC) * T * 2 * n;
     s.total = 2 * s.state + 3 * s.chan + s.bc;
     return s;
 }
@@ -1534,8 +1543,8 @@ kda_status kda_selective_scan_bwd(const void *u, const void *dt, const float *A_
     p.records = space.records;
     p.num_seqs = num_seqs;
     p.D = D; p.n = n; p.G = G;
-    p.cbg = scan_blocks_of_group(D, n, G);
-    p.vec = (D / G) % scan_elems(n) == 0 && all_aligned({u, dt, z, dout, du, ddt, dz});
+    p.cbg = scan_blocks_of_group(D, n, G, kda::kBackKC);
+    p.vec = (D / G) % 2 == 0 && all_aligned({u, dt, z, dout, du, ddt, dz});
     p.vecn = n % 4 == 0 && all_aligned({B, C, initial_state, dfinal_state, dinitial_state});
     const int64_t blocks = space.records * G * p.cbg, bc_blocks = (total_tokens * G * 2 * n + 255) / 256;
     const int64_t w_blocks = ((int64_t)D * (n + 2) + 31) / 32;
@@ -1545,16 +1554,18 @@ kda_status kda_selective_scan_bwd(const void *u, const void *dt, const float *A_
         return with_lanes(n, [&](auto lanes) {
             constexpr bool kBf16 = decltype(bf16)::value;
             constexpr int L = decltype(lanes)::value;
-            constexpr int smem = kda::ScanGradSmem<L>::kBytes;
-            const cudaError_t e = cudaFuncSetAttribute(kda::scan_bwd_grad_kernel<kBf16, L>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            using SM = kda::ScanBwdSmem<kBf16, L>;
+            cudaError_t e = cudaFuncSetAttribute(kda::scan_bwd_chunk_kernel<kBf16, L>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kChunk);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kda::scan_bwd_grad_kernel<kBf16, L>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kGrad);
             if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(selective_scan_bwd)");
-            kda::scan_bwd_chunk_kernel<kBf16, L><<<(unsigned)blocks, kda::kScanThreads, 0, s>>>(p);
+            kda::scan_bwd_chunk_kernel<kBf16, L><<<(unsigned)blocks, kda::kScanThreads, SM::kChunk, s>>>(p);
             const int64_t quads = (int64_t)D * L;
             const dim3 chain((unsigned)((quads + kda::kChainThreads - 1) / kda::kChainThreads),
                              (unsigned)std::min<int32_t>(num_seqs, 65535), 2);
             kda::scan_bwd_chain_kernel<L><<<chain, kda::kChainThreads, 0, s>>>(p);
-            kda::scan_bwd_grad_kernel<kBf16, L><<<(unsigned)blocks, kda::kScanThreads, smem, s>>>(p);
+            kda::scan_bwd_grad_kernel<kBf16, L><<<(unsigned)blocks, kda::kScanThreads, SM::kGrad, s>>>(p);
             if (bc_blocks > 0) kda::scan_bwd_bc_kernel<kBf16><<<(unsigned)bc_blocks, 256, 0, s>>>(p);
             kda::scan_bwd_weights_kernel<<<(unsigned)w_blocks, dim3(32, kda::kColRows), 0, s>>>(p);
             return launched("selective_scan_bwd launch", bc_blocks > 0 ? 5 : 4);
@@ -1594,6 +1605,12 @@ kda_status conv_check(const char *where, int64_t rows, int32_t seqs, int32_t H, 
     if (width < 1 || width > kda::kConvMaxWidth) return fail(KDA_ERR_INVALID_ARG, w + ": width must be in [1, 4]");
     if (!known_dtype(dtype)) return fail(KDA_ERR_INVALID_ARG, w + ": dtype must be KDA_DTYPE_BF16 or KDA_DTYPE_F32");
     return KDA_OK;
+}
+
+// f(integral_constant<bool, b>)
+template <class F>
+kda_status with_flag(bool b, F f) {
+    return b ? f(std::integral_constant<bool, true>()) : f(std::integral_constant<bool, false>());
 }
 
 // f(integral_constant<int, W>)
@@ -1645,7 +1662,7 @@ kda_status kda_short_conv_fwd(const void *x, const float *w, const float *bias, 
         return with_width(width, [&](auto taps) {
             constexpr bool kBf16 = decltype(bf16)::value;
             constexpr int W = decltype(taps)::value, E = kBf16 ? kConvFwdElems16 : kConvFwdElems32;
-            p.vec = C % E == 0 && all_aligned({x, y, initial_state, final_state});
+            const bool vec = C % E == 0 && all_aligned({x, y, initial_state, final_state});
             const int64_t cblocks = conv_channel_blocks(C, E);
             p.run_len = conv_run_len(total_tokens, cblocks, 8, 64);
             p.runs = (total_tokens + p.run_len - 1) / p.run_len;
@@ -1656,12 +1673,15 @@ kda_status kda_short_conv_fwd(const void *x, const float *w, const float *bias, 
             const bool apart = states > 0 && final_state == initial_state && p.runs > 0;
             const int64_t first = apart ? p.runs : p.runs + states;
             if (first == 0) return KDA_OK;
-            kda::conv_state_fwd_kernel<kBf16, W, E><<<dim3((unsigned)first, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
-            if (apart) {
-                p.first_block = p.runs;
-                kda::conv_state_fwd_kernel<kBf16, W, E><<<dim3((unsigned)states, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
-            }
-            return launched("short_conv_fwd launch", apart ? 2 : 1);
+            return with_flag(vec, [&](auto v) {
+                constexpr bool VEC = decltype(v)::value;
+                kda::conv_state_fwd_kernel<kBf16, W, E, VEC><<<dim3((unsigned)first, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
+                if (apart) {
+                    p.first_block = p.runs;
+                    kda::conv_state_fwd_kernel<kBf16, W, E, VEC><<<dim3((unsigned)states, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
+                }
+                return launched("short_conv_fwd launch", apart ? 2 : 1);
+            });
         });
     });
 }
@@ -1694,11 +1714,13 @@ kda_status kda_short_conv_step(const void *x, const float *w, const float *bias,
         return with_width(width, [&](auto taps) {
             constexpr bool kBf16 = decltype(bf16)::value;
             constexpr int W = decltype(taps)::value, E = kBf16 ? kConvFwdElems16 : kConvFwdElems32;
-            p.vec = C % E == 0 && all_aligned({x, y, state});
             const int64_t cblocks = conv_channel_blocks(C, E);
             if (cblocks > 65535) return fail(KDA_ERR_INVALID_ARG, "kda_short_conv_step: too many channels");
-            kda::conv_step_kernel<kBf16, W, E><<<dim3((unsigned)N, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
-            return launched("short_conv_step launch");
+            return with_flag(C % E == 0 && all_aligned({x, y, state}), [&](auto v) {
+                kda::conv_step_kernel<kBf16, W, E, decltype(v)::value>
+                    <<<dim3((unsigned)N, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
+                return launched("short_conv_step launch");
+            });
         });
     });
 }
@@ -1748,7 +1770,7 @@ kda_status kda_short_conv_bwd(const void *x, const float *w, const float *bias, 
     p.num_seqs = num_seqs;
     p.C = (int)C;
     p.d = d;
-    p.vec = C % kConvBwdElems == 0 && all_aligned({x, dy, dx, initial_state, dfinal_state, dinitial_state});
+    const bool vec = C % kConvBwdElems == 0 && all_aligned({x, dy, dx, initial_state, dfinal_state, dinitial_state});
     p.silu = silu != 0;
     p.l2norm = l2norm != 0;
     const int64_t cblocks = conv_channel_blocks(C, kConvBwdElems);
@@ -1757,11 +1779,13 @@ kda_status kda_short_conv_bwd(const void *x, const float *w, const float *bias, 
         return with_width(width, [&](auto taps) {
             constexpr bool kBf16 = decltype(bf16)::value;
             constexpr int W = decltype(taps)::value;
-            kda::conv_state_bwd_kernel<kBf16, W, kConvBwdElems>
-                <<<dim3((unsigned)p.runs, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
-            const int64_t cols = (W + 1) * C;
-            kda::conv_weight_sum_kernel<<<(unsigned)((cols + 31) / 32), dim3(32, kda::kSumRows), 0, s>>>(p.part, p.runs, p.C, W, dw, dbias);
-            return launched("short_conv_bwd launch", 2);
+            return with_flag(vec, [&](auto v) {
+                kda::conv_state_bwd_kernel<kBf16, W, kConvBwdElems, decltype(v)::value>
+                    <<<dim3((unsigned)p.runs, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
+                const int64_t cols = (W + 1) * C;
+                kda::conv_weight_sum_kernel<<<(unsigned)((cols + 31) / 32), dim3(32, kda::kSumRows), 0, s>>>(p.part, p.runs, p.C, W, dw, dbias);
+                return launched("short_conv_bwd launch", 2);
+            });
         });
     });
 }
@@ -1825,11 +1849,12 @@ kda_status kda_layer_norm_fwd(const void *x, const float *w, const float *b, int
             constexpr bool kBf16 = decltype(bf16)::value;
             constexpr int RT = decltype(row_threads)::value, EK = decltype(elems)::value;
             using Block = kda::NormBlock<RT>;
-            p.vec = d % (kBf16 ? 8 : 4) == 0 && all_aligned({x, y});
             const int64_t blocks = (rows + Block::kGroups - 1) / Block::kGroups;
             if (blocks > 0x7fffffffLL) return fail(KDA_ERR_INVALID_ARG, "kda_layer_norm_fwd: too many rows");
-            kda::layer_norm_fwd_kernel<kBf16, RT, EK><<<(unsigned)blocks, Block::kThreads, 0, s>>>(p);
-            return launched("layer_norm_fwd launch");
+            return with_flag(d % (kBf16 ? 8 : 4) == 0 && all_aligned({x, y}), [&](auto vec) {
+                kda::layer_norm_fwd_kernel<kBf16, RT, EK, decltype(vec)::value><<<(unsigned)blocks, Block::kThreads, 0, s>>>(p);
+                return launched("layer_norm_fwd launch");
+            });
         });
     });
 }
@@ -1869,11 +1894,12 @@ kda_status kda_layer_norm_bwd(const void *x, const float *w, const float *mean, 
             constexpr bool kBf16 = decltype(bf16)::value;
             constexpr int RT = decltype(row_threads)::value, EK = decltype(elems)::value;
             using Block = kda::NormBlock<RT>;
-            p.vec = d % (kBf16 ? 8 : 4) == 0 && all_aligned({x, dy, dx});
-            kda::layer_norm_bwd_kernel<kBf16, RT, EK><<<(unsigned)blocks, Block::kThreads, 0, s>>>(p);
-            kda::norm_weight_sum_kernel<<<(unsigned)((2 * d + 31) / 32), dim3(32, kda::kSumRows), 0, s>>>(
-                p.part, blocks * Block::kGroups, d, dw, db);
-            return launched("layer_norm_bwd launch", 2);
+            return with_flag(d % (kBf16 ? 8 : 4) == 0 && all_aligned({x, dy, dx}), [&](auto vec) {
+                kda::layer_norm_bwd_kernel<kBf16, RT, EK, decltype(vec)::value><<<(unsigned)blocks, Block::kThreads, 0, s>>>(p);
+                kda::norm_weight_sum_kernel<<<(unsigned)((2 * d + 31) / 32), dim3(32, kda::kSumRows), 0, s>>>(
+                    p.part, blocks * Block::kGroups, d, dw, db);
+                return launched("layer_norm_bwd launch", 2);
+            });
         });
     });
 }

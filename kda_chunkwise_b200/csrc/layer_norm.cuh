@@ -25,46 +25,27 @@ struct NormParams {
     int64_t rows;
     int d;
     float eps;
-    bool vec;
 };
 
-// elements of a thread: piece k is E consecutive columns (vec), else E columns RT apart
-template <int RT, int E>
-__device__ __forceinline__ int norm_col(int k, int i, int lane, bool vec) {
-    return vec ? (k * RT + lane) * E + i : (k * E + i) * RT + lane;
+// elements of a thread: piece k is E consecutive columns (VEC), else E columns RT apart
+template <int RT, int E, bool VEC>
+__device__ __forceinline__ int norm_col(int k, int i, int lane) {
+    return VEC ? (k * RT + lane) * E + i : (k * E + i) * RT + lane;
 }
 
-template <bool BF16, int RT, int E, int K>
-__device__ __forceinline__ void norm_load(const void *p, int64_t row, int d, int lane, bool vec, bool on, Piece<BF16, E> (&r)[K]) {
+template <bool BF16, int RT, int E, int K, bool VEC>
+__device__ __forceinline__ void norm_load(const void *p, int64_t row, int d, int lane, bool on, Piece<BF16, E> (&r)[K]) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        if (vec) {
-            const int c = norm_col<RT, E>(k, 0, lane, true);
-            load_piece<BF16, E>(p, row * d + c, on && c < d ? E : 0, true, r[k]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int c = norm_col<RT, E>(k, i, lane, false);
-                const bool in = on && c < d;
-                if constexpr (BF16) r[k].w[i] = in ? (uint32_t)__ldg(static_cast<const uint16_t *>(p) + row * d + c) : 0u;
-                else r[k].w[i] = in ? __ldg(static_cast<const uint32_t *>(p) + row * d + c) : 0u;
-            }
-        }
+        const int c = norm_col<RT, E, VEC>(k, 0, lane);
+        load_piece<BF16, E, VEC>(p, row * d + c, !on || c >= d ? 0 : (VEC ? E : (d - c + RT - 1) / RT), r[k], VEC ? 1 : RT);
     }
 }
 
-template <bool BF16, int RT, int E>
-__device__ __forceinline__ void norm_store(void *p, int64_t row, int d, int k, int lane, bool vec, const float (&v)[E]) {
-    if (vec) {
-        const int c = norm_col<RT, E>(k, 0, lane, true);
-        store_piece<BF16, E>(p, row * d + c, c < d ? E : 0, true, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = norm_col<RT, E>(k, i, lane, false);
-            if (c < d) store_out(p, row * d + c, !BF16, v[i]);
-        }
-    }
+template <bool BF16, int RT, int E, bool VEC>
+__device__ __forceinline__ void norm_store(void *p, int64_t row, int d, int k, int lane, const float (&v)[E]) {
+    const int c = norm_col<RT, E, VEC>(k, 0, lane);
+    store_piece<BF16, E, VEC>(p, row * d + c, c >= d ? 0 : (VEC ? E : (d - c + RT - 1) / RT), v, VEC ? 1 : RT);
 }
 
 // Sum of N values over the RT threads of a group.  A group of more than one warp is a whole block;
@@ -96,7 +77,7 @@ struct NormBlock {
     static constexpr int kGroups = kThreads / RT;   // rows a block works on at once
 };
 
-template <bool BF16, int RT, int EK>
+template <bool BF16, int RT, int EK, bool VEC>
 __global__ void __launch_bounds__(NormBlock<RT>::kThreads) layer_norm_fwd_kernel(const NormParams p) {
     constexpr int E = BF16 ? 8 : 4, K = EK / E;
     __shared__ float s_sum[2][RT > 32 ? RT / 32 : 1];
@@ -104,11 +85,11 @@ __global__ void __launch_bounds__(NormBlock<RT>::kThreads) layer_norm_fwd_kernel
     const int64_t row = (int64_t)blockIdx.x * NormBlock<RT>::kGroups + threadIdx.x / RT;
     const bool on = row < p.rows;
     Piece<BF16, E> r[K];
-    norm_load<BF16, RT, E, K>(p.x, row, p.d, lane, p.vec, on, r);
+    norm_load<BF16, RT, E, K, VEC>(p.x, row, p.d, lane, on, r);
     float x[K][E], s[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        piece_to_f32<BF16, E>(r[k], p.vec, x[k]);
+        piece_to_f32<BF16, E, VEC>(r[k], x[k]);
 #pragma unroll
         for (int i = 0; i < E; ++i) s[0] += x[k][i];
     }
@@ -120,7 +101,7 @@ __global__ void __launch_bounds__(NormBlock<RT>::kThreads) layer_norm_fwd_kernel
 #pragma unroll
         for (int i = 0; i < E; ++i) {
             const float c = x[k][i] - mean;
-            if (norm_col<RT, E>(k, i, lane, p.vec) < p.d) s[0] = fmaf(c, c, s[0]);
+            if (norm_col<RT, E, VEC>(k, i, lane) < p.d) s[0] = fmaf(c, c, s[0]);
         }
     norm_sum<RT, 1>(s, s_sum[1]);
     const float rstd = 1.f / sqrtf(s[0] / p.d + p.eps);
@@ -134,14 +115,14 @@ __global__ void __launch_bounds__(NormBlock<RT>::kThreads) layer_norm_fwd_kernel
         float y[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            const int c = norm_col<RT, E>(k, i, lane, p.vec);
+            const int c = norm_col<RT, E, VEC>(k, i, lane);
             y[i] = c < p.d ? fmaf((x[k][i] - mean) * rstd, __ldg(p.w + c), p.b ? __ldg(p.b + c) : 0.f) : 0.f;
         }
-        norm_store<BF16, RT, E>(p.y, row, p.d, k, lane, p.vec, y);
+        norm_store<BF16, RT, E, VEC>(p.y, row, p.d, k, lane, y);
     }
 }
 
-template <bool BF16, int RT, int EK>
+template <bool BF16, int RT, int EK, bool VEC>
 __global__ void __launch_bounds__(NormBlock<RT>::kThreads) layer_norm_bwd_kernel(const NormParams p) {
     constexpr int E = BF16 ? 8 : 4, K = EK / E;
     __shared__ float s_sum[2][RT > 32 ? 2 * (RT / 32) : 1];
@@ -153,7 +134,7 @@ __global__ void __launch_bounds__(NormBlock<RT>::kThreads) layer_norm_bwd_kernel
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            const int c = norm_col<RT, E>(k, i, lane, p.vec);
+            const int c = norm_col<RT, E, VEC>(k, i, lane);
             w[k][i] = c < p.d ? p.w[c] : 0.f;   // zero past d: nothing to the row's sums
             dw[k][i] = db[k][i] = 0.f;
         }
@@ -161,8 +142,8 @@ __global__ void __launch_bounds__(NormBlock<RT>::kThreads) layer_norm_bwd_kernel
     float mean = 0.f, rstd = 0.f;
     auto fetch = [&](int64_t row) {
         const bool on = row < p.rows;
-        norm_load<BF16, RT, E, K>(p.x, row, p.d, lane, p.vec, on, rx);
-        norm_load<BF16, RT, E, K>(p.dy, row, p.d, lane, p.vec, on, rd);
+        norm_load<BF16, RT, E, K, VEC>(p.x, row, p.d, lane, on, rx);
+        norm_load<BF16, RT, E, K, VEC>(p.dy, row, p.d, lane, on, rd);
         mean = on ? p.mean[row] : 0.f;
         rstd = on ? p.rstd[row] : 0.f;
     };
@@ -175,8 +156,8 @@ __global__ void __launch_bounds__(NormBlock<RT>::kThreads) layer_norm_bwd_kernel
         const float m = mean, rs = rstd;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            piece_to_f32<BF16, E>(rx[k], p.vec, xh[k]);
-            piece_to_f32<BF16, E>(rd[k], p.vec, dy[k]);
+            piece_to_f32<BF16, E, VEC>(rx[k], xh[k]);
+            piece_to_f32<BF16, E, VEC>(rd[k], dy[k]);
         }
         if (lead + groups < p.rows) fetch(row + groups);
 #pragma unroll
@@ -198,7 +179,7 @@ __global__ void __launch_bounds__(NormBlock<RT>::kThreads) layer_norm_bwd_kernel
                 float dx[E];
 #pragma unroll
                 for (int i = 0; i < E; ++i) dx[i] = rs * (dy[k][i] - c0 - xh[k][i] * c1);
-                norm_store<BF16, RT, E>(p.y, row, p.d, k, lane, p.vec, dx);
+                norm_store<BF16, RT, E, VEC>(p.y, row, p.d, k, lane, dx);
             }
         }
     }
@@ -206,7 +187,7 @@ __global__ void __launch_bounds__(NormBlock<RT>::kThreads) layer_norm_bwd_kernel
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            const int c = norm_col<RT, E>(k, i, lane, p.vec);
+            const int c = norm_col<RT, E, VEC>(k, i, lane);
             if (c < p.d) {
                 p.part[group * 2 * p.d + c] = dw[k][i];
                 p.part[group * 2 * p.d + p.d + c] = db[k][i];

@@ -8,11 +8,14 @@
 // A prompt takes T D n exponentials and about seven times as many fp32 operations on 4 T D
 // activations: the exponential unit (16 a clock and SM) bounds it, not memory.  So nothing is
 // computed twice that takes an exponential, states stay in registers, and what is per (token,
-// channel) (softplus, the gate) is done once by the thread that stages the value, not once per state.
-//   - A channel's n states lie on L = 2^ceil(log2(n / 4)) lanes, four to a lane; a block of 128 threads
-//     holds 128 / L channels of one group over one segment of one sequence, in tiles of kTT tokens.
-//   - The next tile's activations are in flight in registers while a tile is scanned.
-//   - The sum over m is taken for L tokens at once (transposed_sum): one value a lane.
+// channel) (softplus, the gate) is done once, not once per state.
+//   - A channel's n states lie on L = 2^ceil(log2(n / 4)) lanes, four to a lane; 128 threads scan
+//     KC x 128 / L channels of one group over one segment of one sequence.
+//   - 256 more threads stage the next tile of tokens and write the outputs of the last one meanwhile, so
+//     that the scanning warps only scan: with one sequence there is about one of them per scheduler.
+//   - What a scanning thread reads from shared memory per token is the next bound: B and C lie next to
+//     each other, in bf16 where they came in bf16, and serve the KC channels of a thread.
+//   - The sum over the states is taken for L tokens at once (transposed_sums): one value a lane.
 // Sequences longer than seg_len tokens are cut into segments where the channels alone would leave
 // the GPU empty: a first launch finds every segment's end state from zero and its sum of delta (the
 // decay over a segment is exp(A sum delta)), the second joins those before its own and scans.
@@ -20,19 +23,21 @@
 
 #include "activations.cuh"
 #include "f32x2.cuh"
+#include "mma_frag.cuh"   // cp_async
 
 namespace kda {
 
-constexpr int kScanThreads = 128;
+constexpr int kScanThreads = 128;    // that scan
+constexpr int kStageThreads = 256;   // that stage for them
 
 template <int L>
 struct ScanTile {
     static constexpr int kCH = kScanThreads / L;             // channels of a block
-    static constexpr int kTT = L <= 4 ? 8 * L : 32;          // tokens of a tile
-    static constexpr int kE = kTT * kCH / kScanThreads;      // elements of a tile per thread and tensor
-    static constexpr int kTPR = kCH / kE;                    // threads that stage one row
-    static constexpr int kQ = (kTT * L + kScanThreads - 1) / kScanThreads;   // quads of B (and C) a thread stages
-    static constexpr int kYS = kCH + 32 / L;                 // row stride of the output tile: the lanes' rows fall on different banks
+    static constexpr int kTT = L >= 4 ? 64 : 16 * L;         // tokens of a tile
+    static constexpr int kFR = kCH / 4;                      // fours of channels of a row
+    static constexpr int kR = (kTT * kFR + kStageThreads - 1) / kStageThreads;   // of them a staging thread holds
+    static constexpr int kQ = (kTT * L + kStageThreads - 1) / kStageThreads;     // fours of states of B (and C) it holds
+    static constexpr int kYS = kCH + (L == 16 ? 4 : 32 / L); // row stride of outputs: the lanes' rows fall on different banks
 };
 
 struct ScanParams {
@@ -49,7 +54,7 @@ struct ScanParams {
     int num_seqs, D, n, G;
     int cbg;                            // channel blocks of a group
     int64_t seg_len;
-    bool vec;                           // rows of u, dt, z and out start on kE-element boundaries
+    bool vec;                           // channels of u, dt, z and out may be moved in fours
     bool vecn;                          // n is a multiple of four
 };
 
@@ -99,23 +104,178 @@ __device__ __forceinline__ void store_quad(float *row, int m0, int n, bool vecn,
     }
 }
 
-// A log2(e) for four states; zero past n (a decay of one on states that stay zero)
-__device__ __forceinline__ void load_decay(const float *A_log, int64_t c, int m0, int n, bool active, float (&A2)[4]) {
+// A log2(e) of N states; zero past n (a decay of one on states that stay zero)
+template <int N>
+__device__ __forceinline__ void load_decay(const float *A_log, int64_t c, int m0, int n, bool active, float (&A2)[N]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) A2[i] = active && m0 + i < n ? -1.4426950408889634f * expf(A_log[c * n + m0 + i]) : 0.f;
+    for (int i = 0; i < N; ++i) A2[i] = active && m0 + i < n ? -1.4426950408889634f * expf(A_log[c * n + m0 + i]) : 0.f;
 }
 
 __device__ __forceinline__ float silu(float x) { return x * sigmoid_fast(x); }
 
-template <bool BF16, int L, bool SUMMARY>
-__global__ void __launch_bounds__(kScanThreads) scan_fwd_kernel(const ScanParams p) {
-    using Tile = ScanTile<L>;
-    constexpr int CH = Tile::kCH, TT = Tile::kTT, E = Tile::kE, Q = Tile::kQ, YS = Tile::kYS;
-    __shared__ float4 s_d[TT * CH];                       // delta, delta, delta u, delta u
-    __shared__ __align__(16) float s_B[TT * 4 * L], s_C[SUMMARY ? 4 : TT * 4 * L];
-    __shared__ float s_y[SUMMARY ? 1 : TT * YS];
+// Two neighbouring channels of a row, raw; `on`: how many of the two exist.  bf16 goes as one word where vec
+// allows it.  (Each way of loading has its own registers: two loads into one would wait for each other.)
+template <bool BF16> struct Pair;
+template <> struct Pair<true> {
+    uint32_t v, e[2];
+    __device__ __forceinline__ void load(const void *p, int64_t off, int on, bool vec) {
+        const uint16_t *src = static_cast<const uint16_t *>(p) + off;
+        v = e[0] = e[1] = 0u;
+        load_if<4, true>(src, vec && on > 0, &v);
+        load_if<2, true>(src, !vec && on > 0, &e[0]);
+        load_if<2, true>(src + 1, !vec && on > 1, &e[1]);
+    }
+    __device__ __forceinline__ float2 get(bool vec) const {
+        return make_float2(__uint_as_float((vec ? v : e[0]) << 16), __uint_as_float(vec ? v & 0xFFFF0000u : e[1] << 16));
+    }
+    __device__ __forceinline__ static void store(void *p, int64_t off, int on, bool vec, float x, float y) {
+        uint16_t *dst = static_cast<uint16_t *>(p) + off;
+        if (vec && on > 0) {
+            *reinterpret_cast<uint32_t *>(dst) = pack2_bf16(x, y);
+        } else {
+            if (on > 0) dst[0] = f32_to_bf16(x);
+            if (on > 1) dst[1] = f32_to_bf16(y);
+        }
+    }
+};
+template <> struct Pair<false> {
+    uint32_t e[2];
+    __device__ __forceinline__ void load(const void *p, int64_t off, int on, bool) {
+        const float *src = static_cast<const float *>(p) + off;
+        e[0] = e[1] = 0u;
+        load_if<4, true>(src, on > 0, &e[0]);
+        load_if<4, true>(src + 1, on > 1, &e[1]);
+    }
+    __device__ __forceinline__ float2 get(bool) const { return make_float2(__uint_as_float(e[0]), __uint_as_float(e[1])); }
+    __device__ __forceinline__ static void store(void *p, int64_t off, int on, bool vec, float x, float y) {
+        float *dst = static_cast<float *>(p) + off;
+        if (vec && on > 0) {
+            *reinterpret_cast<float2 *>(dst) = make_float2(x, y);
+        } else {
+            if (on > 0) dst[0] = x;
+            if (on > 1) dst[1] = y;
+        }
+    }
+};
 
-    const int tid = threadIdx.x;
+// Four neighbouring states' values of B or C, raw; `on`: how many exist.
+template <bool BF16> struct Quad;
+template <> struct Quad<true> {
+    uint32_t v[2], e[4];
+    __device__ __forceinline__ void load(const void *p, int64_t off, int on, bool vec) {
+        const uint16_t *src = static_cast<const uint16_t *>(p) + off;
+        v[0] = v[1] = e[0] = e[1] = e[2] = e[3] = 0u;
+        load_if<8, true>(src, vec && on > 0, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_if<2, true>(src + i, !vec && on > i, &e[i]);
+    }
+    __device__ __forceinline__ uint2 get(bool vec) const {
+        return vec ? make_uint2(v[0], v[1]) : make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+    }
+};
+template <> struct Quad<false> {
+    uint32_t e[4];
+    __device__ __forceinline__ void load(const void *p, int64_t off, int on, bool) {
+        const float *src = static_cast<const float *>(p) + off;
+        e[0] = e[1] = e[2] = e[3] = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_if<4, true>(src + i, on > i, &e[i]);
+    }
+    __device__ __forceinline__ float4 get(bool) const {
+        return make_float4(__uint_as_float(e[0]), __uint_as_float(e[1]), __uint_as_float(e[2]), __uint_as_float(e[3]));
+    }
+};
+
+// Four states' B and C of one token, as they lie in shared memory: bf16 as it came, else fp32.
+template <bool BF16> struct QuadBC;
+template <> struct QuadBC<true> {
+    uint2 b, c;
+    __device__ __forceinline__ static f32x2 two(uint32_t w) { return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+    __device__ __forceinline__ static void get(const uint2 &v, f32x2 &lo, f32x2 &hi) { lo = two(v.x); hi = two(v.y); }
+};
+template <> struct QuadBC<false> {
+    float4 b, c;
+    __device__ __forceinline__ static void get(const float4 &v, f32x2 &lo, f32x2 &hi) { lo = f2_pack(v.x, v.y); hi = f2_pack(v.z, v.w); }
+};
+
+// both at once: one 16-byte load for bf16
+__device__ __forceinline__ QuadBC<true> load_bc(const QuadBC<true> *p) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    QuadBC<true> q;
+    q.b = make_uint2(v.x, v.y);
+    q.c = make_uint2(v.z, v.w);
+    return q;
+}
+__device__ __forceinline__ QuadBC<false> load_bc(const QuadBC<false> *p) { return *p; }
+
+// the decays exp(A delta) of four states (single products: a pair would need delta twice in registers)
+__device__ __forceinline__ void decays(const float (&A2)[4], float delta, f32x2 &a01, f32x2 &a23) {
+    a01 = f2_pack(ex2_approx(A2[0] * delta), ex2_approx(A2[1] * delta));
+    a23 = f2_pack(ex2_approx(A2[2] * delta), ex2_approx(A2[3] * delta));
+}
+
+template <bool BF16, int L>
+struct ScanSmem {
+    using Tile = ScanTile<L>;
+    static constexpr int kD = Tile::kTT * Tile::kCH;       // float2 (delta, delta u)
+    static constexpr int kBC = Tile::kTT * L;              // QuadBC
+    static constexpr int kY = Tile::kTT * Tile::kYS;       // float
+    static constexpr int kBuf = kD * 8 + kBC * (int)sizeof(QuadBC<BF16>) + kY * 4;   // of one tile being scanned
+    static constexpr int kFour = BF16 ? 8 : 16;            // bytes of four raw elements
+    static constexpr int kRaw = kStageThreads * (3 * Tile::kR * kFour + Tile::kQ * (int)sizeof(QuadBC<BF16>));   // of one tile on its way
+    static constexpr int kStages = 3;
+    static constexpr int kBytes = 2 * kBuf + kStages * kRaw;
+};
+
+// Asynchronous copy of four elements to shared memory, or zeros past `on` of them.  bf16 that may not be
+// moved as a vector is read and stored at once.
+template <bool BF16>
+__device__ __forceinline__ void copy_four(void *dst, const void *p, int64_t off, int on, bool vec) {
+    constexpr int kElem = BF16 ? 2 : 4, kBytes = 4 * kElem;
+    const char *src = static_cast<const char *>(p) + (on > 0 ? off * kElem : 0);
+    const uint32_t to = smem_u32(dst);
+    if (vec) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(to), "l"(src), "n"(kBytes), "r"(on > 0 ? kBytes : 0) : "memory");
+    } else if constexpr (!BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(to + 4 * i), "l"(src + (on > i ? 4 * i : 0)), "r"(on > i ? 4 : 0) : "memory");
+    } else {
+        uint16_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = on > i ? reinterpret_cast<const uint16_t *>(src)[i] : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) static_cast<uint16_t *>(dst)[i] = v[i];
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void raw_four(const void *p, float (&v)[4]) {
+    if constexpr (BF16) {
+        const uint2 w = *static_cast<const uint2 *>(p);
+        v[0] = __uint_as_float(w.x << 16);
+        v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(w.y << 16);
+        v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    } else {
+        const float4 w = *static_cast<const float4 *>(p);
+        v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+    }
+}
+
+// Threads 0 .. 127 scan, 128 .. 383 stage; one barrier a tile.  While tile i is scanned, the outputs of tile i - 1
+// are written, tile i + 1 is converted and the tiles after it are on their way into a ring (every
+// staging thread reads back what it copied itself).
+template <bool BF16, int L, bool SUMMARY>
+__global__ void __launch_bounds__(kScanThreads + kStageThreads, 1) scan_fwd_kernel(const ScanParams p) {
+    using Tile = ScanTile<L>;
+    using SM = ScanSmem<BF16, L>;
+    constexpr int CH = Tile::kCH, TT = Tile::kTT, R = Tile::kR, Q = Tile::kQ, YS = Tile::kYS, FR = Tile::kFR, NS = SM::kStages;
+    extern __shared__ __align__(16) unsigned char scan_tiles[];
+    auto buf_bc = [&](int b) { return reinterpret_cast<QuadBC<BF16> *>(scan_tiles + b * SM::kBuf); };
+    auto buf_d = [&](int b) { return reinterpret_cast<float2 *>(buf_bc(b) + SM::kBC); };
+    auto buf_y = [&](int b) { return reinterpret_cast<float *>(buf_d(b) + SM::kD); };
+
     if (blockIdx.x == 0 && !SUMMARY) check_seqlens(p.cu, p.num_seqs, p.total_tokens);
     const int ncb = p.G * p.cbg;
     const int64_t rec = blockIdx.x / ncb;
@@ -126,20 +286,133 @@ __global__ void __launch_bounds__(kScanThreads) scan_fwd_kernel(const ScanParams
     bool last;
     if (!scan_segment(p.cu, p.num_seqs, p.total_tokens, p.seg_len, rec, seq, j, t0, t1, last)) return;
     if (SUMMARY && last) return;
+    const int64_t c0 = (int64_t)g * DG + cbase;
+    const int tiles = static_cast<int>((t1 - t0 + TT - 1) / TT);
 
-    // scan role: channel and states of this thread
-    const int lane = tid % L, chl = tid / L, m0 = 4 * lane;
+    if (threadIdx.x >= kScanThreads) {
+        // ---- staging ----
+        const int tid = threadIdx.x - kScanThreads;
+        // four i of this thread: its row, and the channels within the block (the same for every i)
+        auto row_of = [&](int i) { return tid / FR + i * (kStageThreads / FR); };   // (past the tile where there are more threads than fours)
+        const int col = 4 * (tid % FR), left = DG - cbase - col, four_on = left > 0 ? (left > 4 ? 4 : left) : 0;
+        auto on_of = [&](int i, int64_t t) { return t < t1 && row_of(i) < TT ? four_on : 0; };   // how many of them exist at token t
+        float bias[4], skip[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            bias[k] = p.dt_bias && four_on > k ? p.dt_bias[c0 + col + k] : 0.f;
+            skip[k] = p.skip && four_on > k ? p.skip[c0 + col + k] : 0.f;
+        }
+        // this thread's part of a ring slot: fours of u, dt and z, and of B and C
+        unsigned char *ring = scan_tiles + 2 * SM::kBuf;
+        auto raw = [&](int tile, int which) {
+            return ring + (tile % NS) * SM::kRaw + (which * kStageThreads + tid) * SM::kFour;
+        };
+        auto raw_bc = [&](int tile, int q) {
+            return reinterpret_cast<QuadBC<BF16> *>(ring + (tile % NS) * SM::kRaw + 3 * R * kStageThreads * SM::kFour) + q * kStageThreads + tid;
+        };
+        auto fetch = [&](int tile) {
+            const int64_t t = t0 + (int64_t)tile * TT;
+            if (tile < tiles) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const int64_t tt = t + row_of(i), off = tt * p.D + c0 + col;
+                    const int on = on_of(i, tt);
+                    copy_four<BF16>(raw(tile, 3 * i), p.u, off, on, p.vec);
+                    copy_four<BF16>(raw(tile, 3 * i + 1), p.dt, off, on, p.vec);
+                    if (!SUMMARY && p.z) copy_four<BF16>(raw(tile, 3 * i + 2), p.z, off, on, p.vec);
+                }
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    const int i = tid + q * kStageThreads;   // row i / L, states 4 (i % L) ..
+                    const int64_t tb = t + i / L;
+                    const int mm = 4 * (i % L);
+                    int v4 = p.n - mm;
+                    v4 = (i < TT * L && tb < t1 && v4 > 0) ? (v4 > 4 ? 4 : v4) : 0;
+                    copy_four<BF16>(&raw_bc(tile, q)->b, p.B, (tb * p.G + g) * p.n + mm, v4, p.vecn);
+                    if (!SUMMARY) copy_four<BF16>(&raw_bc(tile, q)->c, p.C, (tb * p.G + g) * p.n + mm, v4, p.vecn);
+                }
+            }
+            cp_async_commit();
+        };
+        auto convert = [&](int tile) {
+            const int64_t t = t0 + (int64_t)tile * TT;
+            float2 *d = buf_d(tile & 1);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                if (row_of(i) >= TT) break;
+                const int on = on_of(i, t + row_of(i));
+                float u[4], dt[4];
+                raw_four<BF16>(raw(tile, 3 * i), u);
+                raw_four<BF16>(raw(tile, 3 * i + 1), dt);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) dt[k] = on > k ? softplus(dt[k] + bias[k]) : 0.f;   // zero: the state passes unchanged
+                float4 *dst = reinterpret_cast<float4 *>(&d[row_of(i) * CH + col]);
+                dst[0] = make_float4(dt[0], dt[0] * u[0], dt[1], dt[1] * u[1]);
+                dst[1] = make_float4(dt[2], dt[2] * u[2], dt[3], dt[3] * u[3]);
+            }
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int i = tid + q * kStageThreads;
+                if (i < TT * L) {
+                    if constexpr (SUMMARY) buf_bc(tile & 1)[i].b = raw_bc(tile, q)->b;
+                    else buf_bc(tile & 1)[i] = *raw_bc(tile, q);
+                }
+            }
+        };
+        auto write_out = [&](int tile) {
+            if constexpr (!SUMMARY) {
+                const int64_t t = t0 + (int64_t)tile * TT;
+                const float *y = buf_y(tile & 1);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const int64_t tt = t + row_of(i);
+                    const int on = on_of(i, tt);
+                    if (on == 0) continue;
+                    const float4 yv = *reinterpret_cast<const float4 *>(&y[row_of(i) * YS + col]);
+                    float o[4] = {yv.x, yv.y, yv.z, yv.w}, r[4];
+                    if (p.skip) {
+                        raw_four<BF16>(raw(tile, 3 * i), r);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) o[k] = fmaf(skip[k], r[k], o[k]);
+                    }
+                    if (p.z) {
+                        raw_four<BF16>(raw(tile, 3 * i + 2), r);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) o[k] *= silu(r[k]);
+                    }
+                    if (p.vec) store_piece<BF16, 4, true>(p.out, tt * p.D + c0 + col, on, o);
+                    else store_piece<BF16, 4, false>(p.out, tt * p.D + c0 + col, on, o);
+                }
+            }
+        };
+        for (int i = 0; i + 1 < NS; ++i) fetch(i);
+        cp_async_wait_group<NS - 2>();
+        if (tiles > 0) convert(0);
+        __syncthreads();
+        for (int i = 0; i < tiles; ++i) {   // tile i is being scanned
+            if (i > 0) write_out(i - 1);    // the last use of that tile's slot
+            fetch(i - 1 + NS);
+            cp_async_wait_group<NS - 2>();  // tile i + 1 has landed
+            if (i + 1 < tiles) convert(i + 1);
+            __syncthreads();
+        }
+        cp_async_wait_all();
+        if (tiles > 0) write_out(tiles - 1);
+        return;
+    }
+
+    // ---- scanning: four states of one channel ----
+    const int tid = threadIdx.x, lane = tid % L, chl = tid / L, m0 = 4 * lane;
     const bool active = cbase + chl < DG;
-    const int64_t c = (int64_t)g * DG + cbase + chl;
-    const int64_t row_s = ((int64_t)seq * p.D + c) * p.n;
-    float A2[4], h[4] = {0.f, 0.f, 0.f, 0.f};
+    const int64_t c = c0 + chl, row_s = ((int64_t)seq * p.D + c) * p.n;
+    float A2[4], hv[4] = {0.f, 0.f, 0.f, 0.f}, sum_delta = 0.f;
     load_decay(p.A_log, c, m0, p.n, active, A2);
     if (active) {
         if (j == 0) {
             // with several segments, hN of the last one may be written over h0 while this block runs
             const float *src = (SUMMARY || last) ? p.h0 : p.seg_h0;
-            if (p.h0) load_quad(src + row_s, m0, p.n, p.vecn, h);
-            if (SUMMARY && p.h0) store_quad(p.seg_h0 + row_s, m0, p.n, p.vecn, h);
+            if (p.h0) load_quad(src + row_s, m0, p.n, p.vecn, hv);
+            if (SUMMARY && p.h0) store_quad(p.seg_h0 + row_s, m0, p.n, p.vecn, hv);
         } else if (!SUMMARY) {   // join the segments before this one
             for (int64_t i = 0; i < j; ++i) {
                 const int64_t r = rec - j + i;
@@ -147,125 +420,78 @@ __global__ void __launch_bounds__(kScanThreads) scan_fwd_kernel(const ScanParams
                 load_quad(p.seg_h + (r * p.D + c) * p.n, m0, p.n, p.vecn, e);
                 const float sum = p.seg_delta[r * p.D + c];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) h[k] = fmaf(i > 0 ? ex2_approx(A2[k] * sum) : 0.f, h[k], e[k]);
+                for (int w = 0; w < 4; ++w) hv[w] = fmaf(i > 0 ? ex2_approx(A2[w] * sum) : 0.f, hv[w], e[w]);
             }
         }
     }
-    f32x2 A01 = f2_pack(A2[0], A2[1]), A23 = f2_pack(A2[2], A2[3]);
-    f32x2 h01 = f2_pack(h[0], h[1]), h23 = f2_pack(h[2], h[3]);
-    float sum_delta = 0.f;
-
-    // staging role: E consecutive channels of one row of a tile
-    const int srow = tid / Tile::kTPR, scol = (tid % Tile::kTPR) * E;
-    const int64_t sc = (int64_t)g * DG + cbase + scol;
-    int left = DG - cbase - scol;
-    left = left < 0 ? 0 : (left > E ? E : left);
-    float bias[E], skip[E];
+    f32x2 h01 = f2_pack(hv[0], hv[1]), h23 = f2_pack(hv[2], hv[3]);
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+        const float2 *d = buf_d(i & 1) + chl;
+        const QuadBC<BF16> *bc = buf_bc(i & 1) + lane;
+        float *sy = buf_y(i & 1) + chl;
+        // groups of U tokens, whose outputs are summed over the states together; tokens past the end have
+        // delta = 0 and leave the state as it is
+        constexpr int U = L < 4 ? 4 : L, N = (TT < 32 ? TT : 32) / U;
+        const int groups = static_cast<int>((min64(TT, t1 - t0 - (int64_t)i * TT) + U - 1) / U);
+        auto group = [&](int grp, float (&y)[U]) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        bias[i] = i < left && p.dt_bias ? p.dt_bias[sc + i] : 0.f;
-        skip[i] = !SUMMARY && i < left && p.skip ? p.skip[sc + i] : 0.f;
-    }
-    Piece<BF16, E> ru, rdt, rz;
-    Piece<BF16, 4> rB[Q], rC[SUMMARY ? 1 : Q];
-    auto fetch = [&](int64_t t) {
-        const int64_t tt = t + srow;
-        const int v = tt < t1 ? left : 0;
-        load_piece<BF16, E>(p.u, tt * p.D + sc, v, p.vec, ru);
-        load_piece<BF16, E>(p.dt, tt * p.D + sc, v, p.vec, rdt);
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const int i = tid + q * kScanThreads;   // row i / L, states 4 (i % L) ..
-            const int64_t tb = t + i / L;
-            const int mm = 4 * (i % L);
-            int v4 = p.n - mm;
-            v4 = (i < TT * L && tb < t1 && v4 > 0) ? (v4 > 4 ? 4 : v4) : 0;
-            load_piece<BF16, 4>(p.B, (tb * p.G + g) * p.n + mm, v4, p.vecn, rB[q]);
-            if constexpr (!SUMMARY) load_piece<BF16, 4>(p.C, (tb * p.G + g) * p.n + mm, v4, p.vecn, rC[q]);
-        }
-    };
-
-    fetch(t0);
-    for (int64_t t = t0; t < t1; t += TT) {
-        // stage the tile
-        float u[E];
-        {
-            float dt[E];
-            piece_to_f32<BF16, E>(ru, p.vec, u);
-            piece_to_f32<BF16, E>(rdt, p.vec, dt);
-            const bool row_in = t + srow < t1;
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float d = row_in && i < left ? softplus(dt[i] + bias[i]) : 0.f;   // zero: the state passes unchanged
-                s_d[srow * CH + scol + i] = make_float4(d, d, d * u[i], d * u[i]);
-            }
-#pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                const int i = tid + q * kScanThreads;
-                if (i < TT * L) {
-                    float v[4];
-                    piece_to_f32<BF16, 4>(rB[q], p.vecn, v);
-                    *reinterpret_cast<float4 *>(&s_B[4 * i]) = make_float4(v[0], v[1], v[2], v[3]);
-                    if constexpr (!SUMMARY) {
-                        piece_to_f32<BF16, 4>(rC[q], p.vecn, v);
-                        *reinterpret_cast<float4 *>(&s_C[4 * i]) = make_float4(v[0], v[1], v[2], v[3]);
-                    }
-                }
-            }
-        }
-        __syncthreads();
-        if constexpr (!SUMMARY)
-            if (p.z) load_piece<BF16, E>(p.z, (t + srow) * p.D + sc, t + srow < t1 ? left : 0, p.vec, rz);
-        if (t + TT < t1) fetch(t + TT);
-
-        const int steps = static_cast<int>(min64(TT, t1 - t));
-        for (int tb = 0; tb < steps; tb += L) {
-            float y[L];
-#pragma unroll
-            for (int i = 0; i < L; ++i) {
-                const float4 d = s_d[(tb + i) * CH + chl];
-                const float4 b = *reinterpret_cast<const float4 *>(&s_B[((tb + i) * L + lane) * 4]);
-                const f32x2 dd = f2_pack(d.x, d.y), du = f2_pack(d.z, d.w);
-                float a0, a1, a2, a3;
-                f2_unpack(f2_mul(A01, dd), a0, a1);
-                f2_unpack(f2_mul(A23, dd), a2, a3);
-                const f32x2 e01 = f2_pack(ex2_approx(a0), ex2_approx(a1)), e23 = f2_pack(ex2_approx(a2), ex2_approx(a3));
-                h01 = f2_fma(e01, h01, f2_mul(du, f2_pack(b.x, b.y)));
-                h23 = f2_fma(e23, h23, f2_mul(du, f2_pack(b.z, b.w)));
+            for (int x = 0; x < U; ++x) {
+                const int t = grp * U + x;
+                const float2 v = d[t * CH];
+                f32x2 a01, a23, b01, b23, c01, c23;
                 if constexpr (SUMMARY) {
-                    sum_delta += d.x;
+                    QuadBC<BF16>::get(bc[t * L].b, b01, b23);
                 } else {
-                    const float4 cc = *reinterpret_cast<const float4 *>(&s_C[((tb + i) * L + lane) * 4]);
+                    const QuadBC<BF16> q = load_bc(&bc[t * L]);
+                    QuadBC<BF16>::get(q.b, b01, b23);
+                    QuadBC<BF16>::get(q.c, c01, c23);
+                }
+                decays(A2, v.x, a01, a23);
+                const f32x2 du = f2_splat(v.y);
+                h01 = f2_fma(a01, h01, f2_mul(du, b01));
+                h23 = f2_fma(a23, h23, f2_mul(du, b23));
+                if constexpr (SUMMARY) {
+                    sum_delta += v.x;
+                } else {
                     float lo, hi;
-                    f2_unpack(f2_fma(h23, f2_pack(cc.z, cc.w), f2_mul(h01, f2_pack(cc.x, cc.y))), lo, hi);
-                    y[i] = lo + hi;
+                    f2_unpack(f2_fma(h23, c23, f2_mul(h01, c01)), lo, hi);
+                    y[x] = lo + hi;
                 }
             }
-            if constexpr (!SUMMARY) s_y[(tb + lane) * YS + chl] = transposed_sum<L>(y, lane);
+            if constexpr (!SUMMARY) transposed_sums<U, L, 1>(y, lane);
+        };
+        auto put = [&](int grp, const float (&y)[U]) {
+            if constexpr (!SUMMARY) {
+#pragma unroll
+                for (int x = 0; x < U / L; ++x) sy[(grp * U + lane * (U / L) + x) * YS] = y[x];
+            }
+        };
+        int grp = 0;
+#pragma unroll 1
+        for (; grp + N <= groups; grp += N) {   // unrolled, the outputs stored at the end: no store keeps a later load back
+            float y[N][U];
+#pragma unroll
+            for (int x = 0; x < N; ++x) group(grp + x, y[x]);
+#pragma unroll
+            for (int x = 0; x < N; ++x) put(grp + x, y[x]);
+        }
+#pragma unroll 1
+        for (; grp < groups; ++grp) {
+            float y[U];
+            group(grp, y);
+            put(grp, y);
         }
         __syncthreads();
-        if constexpr (!SUMMARY) {
-            if (t + srow < t1 && left > 0) {
-                float o[E], z[E];
-                if (p.z) piece_to_f32<BF16, E>(rz, p.vec, z);
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    o[i] = fmaf(skip[i], u[i], s_y[srow * YS + scol + i]);
-                    if (p.z) o[i] *= silu(z[i]);
-                }
-                store_piece<BF16, E>(p.out, (t + srow) * p.D + sc, left, p.vec, o);
-            }
-        }
     }
-
-    f2_unpack(h01, h[0], h[1]);
-    f2_unpack(h23, h[2], h[3]);
     if (!active) return;
+    f2_unpack(h01, hv[0], hv[1]);
+    f2_unpack(h23, hv[2], hv[3]);
     if constexpr (SUMMARY) {
-        store_quad(p.seg_h + (rec * p.D + c) * p.n, m0, p.n, p.vecn, h);
+        store_quad(p.seg_h + (rec * p.D + c) * p.n, m0, p.n, p.vecn, hv);
         if (lane == 0) p.seg_delta[rec * p.D + c] = sum_delta;
     } else {
-        if (last && p.hN) store_quad(p.hN + row_s, m0, p.n, p.vecn, h);
+        if (last && p.hN) store_quad(p.hN + row_s, m0, p.n, p.vecn, hv);
     }
 }
 
@@ -299,7 +525,7 @@ __global__ void __launch_bounds__(kScanStepThreads) scan_step_kernel(const ScanS
     v4 = active && v4 > 0 ? (v4 > 4 ? 4 : v4) : 0;
     for (int64_t r0 = (int64_t)blockIdx.y * U; r0 < p.N; r0 += (int64_t)gridDim.y * U) {
         float h[U][4], u[U], dt[U], z[U];
-        Piece<BF16, 4> B[U], C[U];
+        Quad<BF16> B[U], C[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int64_t r = r0 + k;
@@ -318,8 +544,8 @@ __global__ void __launch_bounds__(kScanStepThreads) scan_step_kernel(const ScanS
             u[k] = on ? load_elem<BF16>(p.u, r * p.D + c) : 0.f;
             dt[k] = on ? load_elem<BF16>(p.dt, r * p.D + c) : 0.f;
             z[k] = on && p.z ? load_elem<BF16>(p.z, r * p.D + c) : 0.f;
-            load_piece<BF16, 4>(p.B, (r * p.G + g) * p.n + m0, on ? v4 : 0, p.vecn, B[k]);
-            load_piece<BF16, 4>(p.C, (r * p.G + g) * p.n + m0, on ? v4 : 0, p.vecn, C[k]);
+            B[k].load(p.B, (r * p.G + g) * p.n + m0, on ? v4 : 0, p.vecn);
+            C[k].load(p.C, (r * p.G + g) * p.n + m0, on ? v4 : 0, p.vecn);
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
@@ -327,8 +553,13 @@ __global__ void __launch_bounds__(kScanStepThreads) scan_step_kernel(const ScanS
             const bool on = active && r < p.N;
             const float d = softplus(dt[k] + bias), du = d * u[k];
             float b[4], cc[4], y = 0.f;
-            piece_to_f32<BF16, 4>(B[k], p.vecn, b);
-            piece_to_f32<BF16, 4>(C[k], p.vecn, cc);
+            f32x2 lo, hi;
+            QuadBC<BF16>::get(B[k].get(p.vecn), lo, hi);
+            f2_unpack(lo, b[0], b[1]);
+            f2_unpack(hi, b[2], b[3]);
+            QuadBC<BF16>::get(C[k].get(p.vecn), lo, hi);
+            f2_unpack(lo, cc[0], cc[1]);
+            f2_unpack(hi, cc[2], cc[3]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 h[k][i] = fmaf(ex2_approx(A2[i] * d), h[k][i], du * b[i]);

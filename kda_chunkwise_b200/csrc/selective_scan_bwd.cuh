@@ -15,9 +15,10 @@
 //   2. scan_bwd_chain_kernel  the states at the chunk starts (forwards) and the gradients at the chunk
 //                             ends (backwards), in place
 //   3. scan_bwd_grad_kernel   every chunk's gradients: a pass forwards that keeps every eighth state,
-//                             then eight tokens at a time recomputed into registers and run backwards
+//                             then eight tokens at a time recomputed into registers and run backwards;
+//                             du, ddt and the output take the places of u, delta and dy
 //   4. two sums of partial results over channel blocks (dB, dC) and over chunks (the weights)
-// Three exponentials per (token, channel, state); sums are taken in a fixed order, so results do not
+// Under three exponentials per (token, channel, state); sums are taken in a fixed order, so results do not
 // vary between runs.
 #pragma once
 
@@ -43,150 +44,162 @@ struct ScanBwdParams {
     bool vec, vecn;
 };
 
+constexpr int kBackKC = 2;   // channels of a thread: B and C are read, and dB and dC summed over a warp, once for both
+constexpr int kBack = 8;     // tokens recomputed into registers at once
+
 template <int L>
-struct ScanBwdTile : ScanTile<L> {
-    static constexpr int kTC = 2 * ScanTile<L>::kTT;   // tokens of a chunk (two staged tiles)
+struct ScanBwdTile {
+    static constexpr int kStep = kScanThreads / L;
+    static constexpr int kCH = kBackKC * kStep;             // channels of a block
+    static constexpr int kTC = L >= 4 ? 64 : 16 * L;        // tokens of a chunk
+    static constexpr int kPR = kCH / 2;                     // pairs of channels of a row
+    static constexpr int kR = kTC * kPR / kScanThreads;     // pairs of a chunk per thread
+    static constexpr int kYS = kCH + 32 / L;                // row stride: the lanes' rows fall on different banks
 };
 
-// Sum over LANES lanes (STRIDE apart, this one the idx-th) for V values at once: lane idx is left
-// with the totals of v[idx V / LANES] .. in v[0] ..
-template <int V, int LANES, int STRIDE>
-__device__ __forceinline__ void transposed_sums(float (&v)[V], int idx) {
-    static_assert(V % LANES == 0, "a whole number of values a lane");
-    int half = V / 2;
+// Where a block's channels lie and which of a chunk's rows and channel pairs a thread moves.
+template <int L>
+struct ScanBwdPlace {
+    using Tile = ScanBwdTile<L>;
+    int64_t t0, t1, c0;
+    int left;   // channels of the group from c0 on
+    __device__ __forceinline__ int row(int i) const { return threadIdx.x / Tile::kPR + i * (kScanThreads / Tile::kPR); }
+    __device__ __forceinline__ int col() const { return 2 * (threadIdx.x % Tile::kPR); }
+    __device__ __forceinline__ int on(int i) const {   // how many channels of pair i exist
+        const int n = left - col();
+        return t0 + row(i) < t1 && n > 0 ? (n > 2 ? 2 : n) : 0;
+    }
+    __device__ __forceinline__ int64_t off(int i, int D) const { return (t0 + row(i)) * D + c0 + col(); }
+};
+
+// Stages delta, u and dy of the block's channels ([kTC][kYS] each), B and C.  Rows past the end and channels
+// past the group are zero: there a = 1 and every gradient is zero.
+template <bool BF16, int L>
+__device__ __forceinline__ void stage_bwd(const ScanBwdParams &p, const ScanBwdPlace<L> &at, int g, float *s_delta, float *s_u,
+                                          float *s_dy, QuadBC<BF16> *s_bc) {
+    using Tile = ScanBwdTile<L>;
+    constexpr int YS = Tile::kYS, R = Tile::kR, AHEAD = R < 8 ? R : 8;
+    for (int i = threadIdx.x; i < Tile::kTC * L; i += kScanThreads) {   // row i / L, states 4 (i % L) ..
+        const int64_t tb = at.t0 + i / L;
+        const int mm = 4 * (i % L);
+        int v4 = p.n - mm;
+        v4 = tb < at.t1 && v4 > 0 ? (v4 > 4 ? 4 : v4) : 0;
+        Quad<BF16> rB, rC;
+        rB.load(p.B, (tb * p.G + g) * p.n + mm, v4, p.vecn);
+        rC.load(p.C, (tb * p.G + g) * p.n + mm, v4, p.vecn);
+        s_bc[i].b = rB.get(p.vecn);
+        s_bc[i].c = rC.get(p.vecn);
+    }
+    const float b0 = p.dt_bias && at.left > at.col() ? p.dt_bias[at.c0 + at.col()] : 0.f;
+    const float b1 = p.dt_bias && at.left > at.col() + 1 ? p.dt_bias[at.c0 + at.col() + 1] : 0.f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < R; i0 += AHEAD) {
+        Pair<BF16> ru[AHEAD], rdt[AHEAD], rdo[AHEAD], rz[AHEAD];
 #pragma unroll
-    for (int w = LANES / 2; w > 0; w >>= 1) {
-        const bool upper = idx & w;
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            if (i >= half) break;
-            const float keep = upper ? v[i + half] : v[i];
-            const float give = upper ? v[i] : v[i + half];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, w * STRIDE);
+        for (int k = 0; k < AHEAD; ++k) {
+            const int i = i0 + k, on = at.on(i);
+            const int64_t off = at.off(i, p.D);
+            ru[k].load(p.u, off, on, p.vec);
+            rdt[k].load(p.dt, off, on, p.vec);
+            rdo[k].load(p.dout, off, on, p.vec);
+            rz[k].load(p.z, off, p.z ? on : 0, p.vec);
         }
-        half >>= 1;
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int i = i0 + k, on = at.on(i), x = at.row(i) * YS + at.col();
+            const float2 dt = rdt[k].get(p.vec);
+            float2 dy = rdo[k].get(p.vec);
+            if (p.z) {
+                const float2 z = rz[k].get(p.vec);
+                dy.x *= silu(z.x);
+                dy.y *= silu(z.y);
+            }
+            *reinterpret_cast<float2 *>(&s_delta[x]) =
+                make_float2(on > 0 ? softplus(dt.x + b0) : 0.f, on > 1 ? softplus(dt.y + b1) : 0.f);
+            *reinterpret_cast<float2 *>(&s_u[x]) = ru[k].get(p.vec);
+            *reinterpret_cast<float2 *>(&s_dy[x]) = dy;
+        }
     }
 }
 
-// What a chunk's block stages: delta, u and dy of its channels ([rows][kYS] each), B and C
-// ([rows][4 L]).  Rows past t1 and channels past the group are zero: there a = 1 and every gradient
-// is zero.  `row0`: rows of the first staged row in the arrays.
 template <bool BF16, int L>
-__device__ __forceinline__ void stage_bwd(const ScanBwdParams &p, int64_t t, int64_t t1, int g, int cbase, int row0,
-                                          float *s_delta, float *s_u, float *s_dy, float *s_B, float *s_C) {
-    using Tile = ScanTile<L>;
-    constexpr int E = Tile::kE, YS = Tile::kYS;
-    const int tid = threadIdx.x, DG = p.D / p.G;
-    const int srow = tid / Tile::kTPR, scol = (tid % Tile::kTPR) * E;
-    const int64_t sc = (int64_t)g * DG + cbase + scol;
-    int left = DG - cbase - scol;
-    left = left < 0 ? 0 : (left > E ? E : left);
-    const int64_t tt = t + srow;
-    const int v = tt < t1 ? left : 0;
-    Piece<BF16, E> ru, rdt, rdo, rz;
-    load_piece<BF16, E>(p.u, tt * p.D + sc, v, p.vec, ru);
-    load_piece<BF16, E>(p.dt, tt * p.D + sc, v, p.vec, rdt);
-    load_piece<BF16, E>(p.dout, tt * p.D + sc, v, p.vec, rdo);
-    if (p.z) load_piece<BF16, E>(p.z, tt * p.D + sc, v, p.vec, rz);
-    Piece<BF16, 4> rB[Tile::kQ], rC[Tile::kQ];
-#pragma unroll
-    for (int q = 0; q < Tile::kQ; ++q) {
-        const int i = tid + q * kScanThreads;
-        const int64_t tb = t + i / L;
-        const int mm = 4 * (i % L);
-        int v4 = p.n - mm;
-        v4 = (i < Tile::kTT * L && tb < t1 && v4 > 0) ? (v4 > 4 ? 4 : v4) : 0;
-        load_piece<BF16, 4>(p.B, (tb * p.G + g) * p.n + mm, v4, p.vecn, rB[q]);
-        load_piece<BF16, 4>(p.C, (tb * p.G + g) * p.n + mm, v4, p.vecn, rC[q]);
-    }
-    float u[E], dt[E], dy[E];
-    piece_to_f32<BF16, E>(ru, p.vec, u);
-    piece_to_f32<BF16, E>(rdt, p.vec, dt);
-    piece_to_f32<BF16, E>(rdo, p.vec, dy);
-    if (p.z) {
-        float z[E];
-        piece_to_f32<BF16, E>(rz, p.vec, z);
-#pragma unroll
-        for (int i = 0; i < E; ++i) dy[i] *= silu(z[i]);
-    }
-    const int at = (row0 + srow) * YS + scol;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const bool in = i < v;
-        s_delta[at + i] = in ? softplus(dt[i] + (p.dt_bias ? p.dt_bias[sc + i] : 0.f)) : 0.f;
-        s_u[at + i] = u[i];
-        s_dy[at + i] = in ? dy[i] : 0.f;
-    }
-#pragma unroll
-    for (int q = 0; q < Tile::kQ; ++q) {
-        const int i = tid + q * kScanThreads;
-        if (i < Tile::kTT * L) {
-            float b[4], c[4];
-            piece_to_f32<BF16, 4>(rB[q], p.vecn, b);
-            piece_to_f32<BF16, 4>(rC[q], p.vecn, c);
-            *reinterpret_cast<float4 *>(&s_B[row0 * 4 * L + 4 * i]) = make_float4(b[0], b[1], b[2], b[3]);
-            *reinterpret_cast<float4 *>(&s_C[row0 * 4 * L + 4 * i]) = make_float4(c[0], c[1], c[2], c[3]);
-        }
-    }
-}
+struct ScanBwdSmem {
+    using Tile = ScanBwdTile<L>;
+    static constexpr int kAct = Tile::kTC * Tile::kYS * 4;                               // delta, u, dy
+    static constexpr int kBC = Tile::kTC * L * (int)sizeof(QuadBC<BF16>);
+    static constexpr int kChunk = 3 * kAct + kBC;                                        // of the chunk kernel
+    static constexpr int kCkpt = Tile::kTC / kBack * kBackKC * 16 * kScanThreads;        // every eighth state
+    static constexpr int kRed = 2 * (kScanThreads / 32) * kBack * 8 * L * 4;             // two buffers of the warps' dB, dC rows
+    static constexpr int kGrad = kChunk + kCkpt + kRed;
+};
 
 template <bool BF16, int L>
 __global__ void __launch_bounds__(kScanThreads) scan_bwd_chunk_kernel(const ScanBwdParams p) {
     using Tile = ScanBwdTile<L>;
-    constexpr int TT = Tile::kTT, CH = Tile::kCH, YS = Tile::kYS;
-    __shared__ float s_delta[TT * YS], s_u[TT * YS], s_dy[TT * YS];
-    __shared__ __align__(16) float s_B[TT * 4 * L], s_C[TT * 4 * L];
+    using SM = ScanBwdSmem<BF16, L>;
+    constexpr int CH = Tile::kCH, YS = Tile::kYS, KC = kBackKC;
+    extern __shared__ __align__(16) unsigned char scan_smem[];
+    QuadBC<BF16> *s_bc = reinterpret_cast<QuadBC<BF16> *>(scan_smem);
+    float *s_delta = reinterpret_cast<float *>(scan_smem + SM::kBC), *s_u = s_delta + SM::kAct / 4, *s_dy = s_u + SM::kAct / 4;
     const int tid = threadIdx.x, ncb = p.G * p.cbg, cb = blockIdx.x % ncb;
     if (blockIdx.x == 0) check_seqlens(p.cu, p.num_seqs, p.total_tokens);
     const int64_t rec = blockIdx.x / ncb;
     const int DG = p.D / p.G, g = cb / p.cbg, cbase = (cb % p.cbg) * CH;
     int seq;
-    int64_t j, t0, t1;
+    int64_t j;
     bool last;
-    if (!scan_segment(p.cu, p.num_seqs, p.total_tokens, Tile::kTC, rec, seq, j, t0, t1, last)) return;
+    ScanBwdPlace<L> at;
+    at.c0 = (int64_t)g * DG + cbase;
+    at.left = DG - cbase;
+    if (!scan_segment(p.cu, p.num_seqs, p.total_tokens, Tile::kTC, rec, seq, j, at.t0, at.t1, last)) return;
     const int lane = tid % L, chl = tid / L, m0 = 4 * lane;
-    const bool active = cbase + chl < DG;
-    const int64_t c = (int64_t)g * DG + cbase + chl;
-    float A2[4];
-    load_decay(p.A_log, c, m0, p.n, active, A2);
-    const f32x2 A01 = f2_pack(A2[0], A2[1]), A23 = f2_pack(A2[2], A2[3]);
-    f32x2 h01 = 0ull, h23 = 0ull, r01 = 0ull, r23 = 0ull;
-    f32x2 P01 = f2_splat(1.f), P23 = f2_splat(1.f);   // product of the decays so far
-    float sum_delta = 0.f;
-    for (int64_t t = t0; t < t1; t += TT) {
-        if (t > t0) __syncthreads();
-        stage_bwd<BF16, L>(p, t, t1, g, cbase, 0, s_delta, s_u, s_dy, s_B, s_C);
-        __syncthreads();
-        const int steps = static_cast<int>(min64(TT, t1 - t));
+    f32x2 h01[KC], h23[KC], r01[KC], r23[KC], P01[KC], P23[KC];   // P: product of the decays so far
+    float A2[KC][4], sum_delta[KC];
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+        load_decay(p.A_log, at.c0 + chl + k * Tile::kStep, m0, p.n, chl + k * Tile::kStep < at.left, A2[k]);
+        h01[k] = h23[k] = r01[k] = r23[k] = 0ull;
+        P01[k] = P23[k] = f2_splat(1.f);
+        sum_delta[k] = 0.f;
+    }
+    stage_bwd<BF16, L>(p, at, g, s_delta, s_u, s_dy, s_bc);
+    __syncthreads();
+    const int steps = static_cast<int>(at.t1 - at.t0);
 #pragma unroll 4
-        for (int i = 0; i < steps; ++i) {
-            const float d = s_delta[i * YS + chl], u = s_u[i * YS + chl], dy = s_dy[i * YS + chl];
-            const float4 b = *reinterpret_cast<const float4 *>(&s_B[(i * L + lane) * 4]);
-            const float4 cc = *reinterpret_cast<const float4 *>(&s_C[(i * L + lane) * 4]);
-            const f32x2 dd = f2_splat(d), du = f2_splat(d * u), dyy = f2_splat(dy);
-            float a0, a1, a2, a3;
-            f2_unpack(f2_mul(A01, dd), a0, a1);
-            f2_unpack(f2_mul(A23, dd), a2, a3);
-            const f32x2 e01 = f2_pack(ex2_approx(a0), ex2_approx(a1)), e23 = f2_pack(ex2_approx(a2), ex2_approx(a3));
-            h01 = f2_fma(e01, h01, f2_mul(du, f2_pack(b.x, b.y)));
-            h23 = f2_fma(e23, h23, f2_mul(du, f2_pack(b.z, b.w)));
-            P01 = f2_mul(P01, e01);
-            P23 = f2_mul(P23, e23);
-            r01 = f2_fma(P01, f2_mul(dyy, f2_pack(cc.x, cc.y)), r01);
-            r23 = f2_fma(P23, f2_mul(dyy, f2_pack(cc.z, cc.w)), r23);
-            sum_delta += d;
+    for (int i = 0; i < steps; ++i) {
+        const QuadBC<BF16> q = load_bc(&s_bc[i * L + lane]);
+        f32x2 b01, b23, c01, c23;
+        QuadBC<BF16>::get(q.b, b01, b23);
+        QuadBC<BF16>::get(q.c, c01, c23);
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+            const int x = i * YS + chl + k * Tile::kStep;
+            const float d = s_delta[x];
+            const f32x2 du = f2_splat(d * s_u[x]), dy = f2_splat(s_dy[x]);
+            f32x2 a01, a23;
+            decays(A2[k], d, a01, a23);
+            h01[k] = f2_fma(a01, h01[k], f2_mul(du, b01));
+            h23[k] = f2_fma(a23, h23[k], f2_mul(du, b23));
+            P01[k] = f2_mul(P01[k], a01);
+            P23[k] = f2_mul(P23[k], a23);
+            r01[k] = f2_fma(P01[k], f2_mul(dy, c01), r01[k]);
+            r23[k] = f2_fma(P23[k], f2_mul(dy, c23), r23[k]);
+            sum_delta[k] += d;
         }
     }
-    if (!active) return;
-    float h[4], r[4];
-    f2_unpack(h01, h[0], h[1]);
-    f2_unpack(h23, h[2], h[3]);
-    f2_unpack(r01, r[0], r[1]);
-    f2_unpack(r23, r[2], r[3]);
-    const int64_t row = (rec * p.D + c) * p.n;
-    store_quad(p.H + row, m0, p.n, p.vecn, h);
-    store_quad(p.R + row, m0, p.n, p.vecn, r);
-    if (lane == 0) p.sum_delta[rec * p.D + c] = sum_delta;
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+        if (chl + k * Tile::kStep >= at.left) continue;
+        const int64_t c = at.c0 + chl + k * Tile::kStep, row = (rec * p.D + c) * p.n;
+        float h[4], r[4];
+        f2_unpack(h01[k], h[0], h[1]);
+        f2_unpack(h23[k], h[2], h[3]);
+        f2_unpack(r01[k], r[0], r[1]);
+        f2_unpack(r23[k], r[2], r[3]);
+        store_quad(p.H + row, m0, p.n, p.vecn, h);
+        store_quad(p.R + row, m0, p.n, p.vecn, r);
+        if (lane == 0) p.sum_delta[rec * p.D + c] = sum_delta[k];
+    }
 }
 
 constexpr int kChainThreads = 128;
@@ -239,250 +252,244 @@ __global__ void __launch_bounds__(kChainThreads) scan_bwd_chain_kernel(const Sca
     }
 }
 
-constexpr int kBack = 8;   // tokens recomputed into registers at once
-
-template <int L>
-struct ScanGradSmem {
-    using Tile = ScanBwdTile<L>;
-    static constexpr int kAct = Tile::kTC * Tile::kYS;                  // delta, u, dy
-    static constexpr int kBC = Tile::kTC * 4 * L;                       // B, C
-    static constexpr int kCkpt = Tile::kTC / kBack * 4 * kScanThreads;  // every eighth state
-    static constexpr int kRed = 2 * (kScanThreads / 32) * kBack * 8 * L;   // two buffers of the warps' dB, dC rows
-    static constexpr int kY = kAct > kRed ? kAct : kRed;                // the forward pass's outputs, then those rows
-    static constexpr int kBytes = (3 * kAct + 2 * kBC + kCkpt + kY) * 4;
-};
-
 template <bool BF16, int L>
 __global__ void __launch_bounds__(kScanThreads) scan_bwd_grad_kernel(const ScanBwdParams p) {
     using Tile = ScanBwdTile<L>;
-    using SM = ScanGradSmem<L>;
-    constexpr int TT = Tile::kTT, TC = Tile::kTC, CH = Tile::kCH, E = Tile::kE, YS = Tile::kYS;
-    constexpr int KW = 32 / L;               // channels of a warp
+    using SM = ScanBwdSmem<BF16, L>;
+    constexpr int TC = Tile::kTC, CH = Tile::kCH, YS = Tile::kYS, KC = kBackKC;
+    constexpr int KW = 32 / L;               // channels side by side in a warp
     constexpr int TB = KW > 8 ? KW / 8 : 1;  // tokens whose dB, dC rows are summed over the warp at once
     constexpr int VPL = 8 * TB / KW;         // values of them a lane is left with
-    constexpr int YB = L > kBack ? L : kBack;   // tokens whose outputs are summed over the states at once
-    extern __shared__ __align__(16) float scan_smem[];
-    float *s_delta = scan_smem, *s_u = s_delta + SM::kAct, *s_dy = s_u + SM::kAct;
-    float *s_B = s_dy + SM::kAct, *s_C = s_B + SM::kBC;
-    float4 *s_ckpt = reinterpret_cast<float4 *>(s_C + SM::kBC);
-    float *s_y = s_C + SM::kBC + SM::kCkpt, *s_red = s_y;
+    constexpr int RED = kBack * 8 * L;       // dB, dC rows of kBack tokens
+    extern __shared__ __align__(16) unsigned char scan_smem[];
+    QuadBC<BF16> *s_bc = reinterpret_cast<QuadBC<BF16> *>(scan_smem);
+    float *s_delta = reinterpret_cast<float *>(scan_smem + SM::kBC), *s_u = s_delta + SM::kAct / 4, *s_dy = s_u + SM::kAct / 4;
+    float4 *s_ckpt = reinterpret_cast<float4 *>(scan_smem + SM::kChunk);
+    float *s_red = reinterpret_cast<float *>(scan_smem + SM::kChunk + SM::kCkpt);
 
     const int tid = threadIdx.x, ncb = p.G * p.cbg, cb = blockIdx.x % ncb;
     const int64_t rec = blockIdx.x / ncb;
     const int DG = p.D / p.G, g = cb / p.cbg, cbase = (cb % p.cbg) * CH;
     const int lane = tid % L, chl = tid / L, m0 = 4 * lane, warp = tid / 32;
-    const bool active = cbase + chl < DG;
-    const int64_t c = (int64_t)g * DG + cbase + chl;
-    const int64_t row = (rec * p.D + c) * p.n;
     int seq;
-    int64_t j, t0, t1;
+    int64_t j;
     bool last;
-    if (!scan_segment(p.cu, p.num_seqs, p.total_tokens, TC, rec, seq, j, t0, t1, last)) {
-        const float zero[4] = {0.f, 0.f, 0.f, 0.f};   // a record without a chunk: nothing to the weights' sums
-        if (active) {
-            store_quad(p.H + row, m0, p.n, p.vecn, zero);
-            if (lane == 0) p.pskip[rec * p.D + c] = p.pbias[rec * p.D + c] = 0.f;
+    ScanBwdPlace<L> at;
+    at.c0 = (int64_t)g * DG + cbase;
+    at.left = DG - cbase;
+    const bool chunk = scan_segment(p.cu, p.num_seqs, p.total_tokens, TC, rec, seq, j, at.t0, at.t1, last);
+    f32x2 h01[KC], h23[KC], g01[KC], g23[KC];   // g: a_{t+1} g_{t+1}
+    float A2[KC][4];
+    f32x2 dA01[KC], dA23[KC];
+    float skip[KC], dskip[KC], dbias[KC];
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+        const bool active = chl + k * Tile::kStep < at.left;
+        const int64_t c = at.c0 + chl + k * Tile::kStep, row = (rec * p.D + c) * p.n;
+        float h[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f};
+        if (!chunk) {   // a record without a chunk: nothing to the weights' sums
+            if (active) {
+                store_quad(p.H + row, m0, p.n, p.vecn, h);
+                if (lane == 0) p.pskip[rec * p.D + c] = p.pbias[rec * p.D + c] = 0.f;
+            }
+            continue;
         }
-        return;
+        load_decay(p.A_log, c, m0, p.n, active, A2[k]);
+        if (active) {
+            load_quad(p.H + row, m0, p.n, p.vecn, h);
+            load_quad(p.R + row, m0, p.n, p.vecn, r);
+        }
+        h01[k] = f2_pack(h[0], h[1]);
+        h23[k] = f2_pack(h[2], h[3]);
+        g01[k] = f2_pack(r[0], r[1]);
+        g23[k] = f2_pack(r[2], r[3]);
+        dA01[k] = dA23[k] = 0ull;
+        skip[k] = active && p.skip ? p.skip[c] : 0.f;
+        dskip[k] = dbias[k] = 0.f;
     }
-    float A2[4], h[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f};
-    load_decay(p.A_log, c, m0, p.n, active, A2);
-    if (active) {
-        load_quad(p.H + row, m0, p.n, p.vecn, h);
-        load_quad(p.R + row, m0, p.n, p.vecn, r);
-    }
-    const f32x2 A01 = f2_pack(A2[0], A2[1]), A23 = f2_pack(A2[2], A2[3]);
-    f32x2 h01 = f2_pack(h[0], h[1]), h23 = f2_pack(h[2], h[3]);
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k)
-        stage_bwd<BF16, L>(p, t0 + k * TT, t1, g, cbase, k * TT, s_delta, s_u, s_dy, s_B, s_C);
+    if (!chunk) return;
+    stage_bwd<BF16, L>(p, at, g, s_delta, s_u, s_dy, s_bc);
     __syncthreads();
 
-    // forwards: every eighth state, and the outputs where the gate's gradient needs them
+    // forwards: the state before every kBack tokens (read back by the thread that wrote it)
+    const int blocks = static_cast<int>((at.t1 - at.t0 + kBack - 1) / kBack);
 #pragma unroll 1
-    for (int tb = 0; tb < TC; tb += YB) {
-        float y[YB];
+    for (int sb = 0; sb < blocks; ++sb) {
 #pragma unroll
-        for (int i = 0; i < YB; ++i) {
-            if (i % kBack == 0) {
-                float s[4];
-                f2_unpack(h01, s[0], s[1]);
-                f2_unpack(h23, s[2], s[3]);
-                s_ckpt[(tb + i) / kBack * kScanThreads + tid] = make_float4(s[0], s[1], s[2], s[3]);
-            }
-            const float d = s_delta[(tb + i) * YS + chl], u = s_u[(tb + i) * YS + chl];
-            const float4 b = *reinterpret_cast<const float4 *>(&s_B[((tb + i) * L + lane) * 4]);
-            const float4 cc = *reinterpret_cast<const float4 *>(&s_C[((tb + i) * L + lane) * 4]);
-            const f32x2 dd = f2_splat(d), du = f2_splat(d * u);
-            float a0, a1, a2, a3;
-            f2_unpack(f2_mul(A01, dd), a0, a1);
-            f2_unpack(f2_mul(A23, dd), a2, a3);
-            h01 = f2_fma(f2_pack(ex2_approx(a0), ex2_approx(a1)), h01, f2_mul(du, f2_pack(b.x, b.y)));
-            h23 = f2_fma(f2_pack(ex2_approx(a2), ex2_approx(a3)), h23, f2_mul(du, f2_pack(b.z, b.w)));
-            float lo, hi;
-            f2_unpack(f2_fma(h23, f2_pack(cc.z, cc.w), f2_mul(h01, f2_pack(cc.x, cc.y))), lo, hi);
-            y[i] = lo + hi;
+        for (int k = 0; k < KC; ++k) {
+            float s[4];
+            f2_unpack(h01[k], s[0], s[1]);
+            f2_unpack(h23[k], s[2], s[3]);
+            s_ckpt[(sb * KC + k) * kScanThreads + tid] = make_float4(s[0], s[1], s[2], s[3]);
         }
-        if (p.z) {
-            transposed_sums<YB, L, 1>(y, lane);
+        if (sb + 1 == blocks) break;
 #pragma unroll
-            for (int k = 0; k < YB / L; ++k) s_y[(tb + lane * (YB / L) + k) * YS + chl] = y[k];
-        }
-    }
-    const int srow = tid / Tile::kTPR, scol = (tid % Tile::kTPR) * E;
-    const int64_t sc = (int64_t)g * DG + cbase + scol;
-    int left = DG - cbase - scol;
-    left = left < 0 ? 0 : (left > E ? E : left);
-    if (p.z) {
-        __syncthreads();
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-            const int64_t tt = t0 + k * TT + srow;
-            if (tt < t1 && left > 0) {
-                Piece<BF16, E> rz, rdo;
-                float z[E], o[E];
-                load_piece<BF16, E>(p.z, tt * p.D + sc, left, p.vec, rz);
-                load_piece<BF16, E>(p.dout, tt * p.D + sc, left, p.vec, rdo);
-                piece_to_f32<BF16, E>(rz, p.vec, z);
-                piece_to_f32<BF16, E>(rdo, p.vec, o);
-                const int at = (k * TT + srow) * YS + scol;
+        for (int i = 0; i < kBack; ++i) {
+            f32x2 b01, b23;
+            QuadBC<BF16>::get(s_bc[(sb * kBack + i) * L + lane].b, b01, b23);
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const float y = fmaf(i < left && p.skip ? p.skip[sc + i] : 0.f, s_u[at + i], s_y[at + i]);
-                    const float s = sigmoid_fast(z[i]);
-                    o[i] *= y * s * fmaf(z[i], 1.f - s, 1.f);
-                }
-                store_piece<BF16, E>(p.dz, tt * p.D + sc, left, p.vec, o);
+            for (int k = 0; k < KC; ++k) {
+                const int x = (sb * kBack + i) * YS + chl + k * Tile::kStep;
+                const float d = s_delta[x];
+                const f32x2 du = f2_splat(d * s_u[x]);
+                f32x2 a01, a23;
+                decays(A2[k], d, a01, a23);
+                h01[k] = f2_fma(a01, h01[k], f2_mul(du, b01));
+                h23[k] = f2_fma(a23, h23[k], f2_mul(du, b23));
             }
         }
-        __syncthreads();   // s_red takes the place of s_y
     }
 
     // backwards
-    const float skip = active && p.skip ? p.skip[c] : 0.f;
-    f32x2 g01 = f2_pack(r[0], r[1]), g23 = f2_pack(r[2], r[3]);   // a_{t+1} g_{t+1}
-    f32x2 dA01 = 0ull, dA23 = 0ull;
-    float dskip = 0.f, dbias = 0.f;
 #pragma unroll 1
-    for (int sb = TC / kBack - 1; sb >= 0; --sb) {
+    for (int sb = blocks - 1; sb >= 0; --sb) {
         const int tb = sb * kBack;
-        f32x2 a01[kBack], a23[kBack], p01[kBack], p23[kBack];   // a_t and a_t h_{t-1}
-        {
-            const float4 s = s_ckpt[sb * kScanThreads + tid];
-            h01 = f2_pack(s.x, s.y);
-            h23 = f2_pack(s.z, s.w);
+        f32x2 a01[kBack][KC], a23[kBack][KC], p01[kBack][KC], p23[kBack][KC];   // a_t and a_t h_{t-1}
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+            const float4 s = s_ckpt[(sb * KC + k) * kScanThreads + tid];
+            h01[k] = f2_pack(s.x, s.y);
+            h23[k] = f2_pack(s.z, s.w);
         }
 #pragma unroll
         for (int i = 0; i < kBack; ++i) {
-            const float d = s_delta[(tb + i) * YS + chl], u = s_u[(tb + i) * YS + chl];
-            const float4 b = *reinterpret_cast<const float4 *>(&s_B[((tb + i) * L + lane) * 4]);
-            const f32x2 dd = f2_splat(d), du = f2_splat(d * u);
-            float x0, x1, x2, x3;
-            f2_unpack(f2_mul(A01, dd), x0, x1);
-            f2_unpack(f2_mul(A23, dd), x2, x3);
-            a01[i] = f2_pack(ex2_approx(x0), ex2_approx(x1));
-            a23[i] = f2_pack(ex2_approx(x2), ex2_approx(x3));
-            p01[i] = f2_mul(a01[i], h01);
-            p23[i] = f2_mul(a23[i], h23);
-            h01 = f2_fma(du, f2_pack(b.x, b.y), p01[i]);
-            h23 = f2_fma(du, f2_pack(b.z, b.w), p23[i]);
+            f32x2 b01, b23;
+            QuadBC<BF16>::get(s_bc[(tb + i) * L + lane].b, b01, b23);
+#pragma unroll
+            for (int k = 0; k < KC; ++k) {
+                const int x = (tb + i) * YS + chl + k * Tile::kStep;
+                const float d = s_delta[x];
+                const f32x2 du = f2_splat(d * s_u[x]);
+                decays(A2[k], d, a01[i][k], a23[i][k]);
+                p01[i][k] = f2_mul(a01[i][k], h01[k]);
+                p23[i][k] = f2_mul(a23[i][k], h23[k]);
+                h01[k] = f2_fma(du, b01, p01[i][k]);
+                h23[k] = f2_fma(du, b23, p23[i][k]);
+            }
         }
-        float *red = s_red + (sb & 1) * ((kScanThreads / 32) * kBack * 8 * L) + warp * (kBack * 8 * L);
-        float v[2 * kBack];
+        float *red = s_red + (sb & 1) * (kScanThreads / 32 * RED) + warp * RED;
+        // sums over a channel's states: of g B (the gradient of delta u), of e A (of delta), and the output
+        constexpr int NV = L > kBack ? 4 : 3;   // (16 lanes: four a token, so that two lanes hold one)
+        float v[KC][NV * kBack];
         float bc[8 * TB];
 #pragma unroll
         for (int i = kBack - 1; i >= 0; --i) {
-            const float d = s_delta[(tb + i) * YS + chl], u = s_u[(tb + i) * YS + chl], dy = s_dy[(tb + i) * YS + chl];
-            const float4 b = *reinterpret_cast<const float4 *>(&s_B[((tb + i) * L + lane) * 4]);
-            const float4 cc = *reinterpret_cast<const float4 *>(&s_C[((tb + i) * L + lane) * 4]);
-            const f32x2 b01 = f2_pack(b.x, b.y), b23 = f2_pack(b.z, b.w);
-            const f32x2 dd = f2_splat(d), du = f2_splat(d * u), dyy = f2_splat(dy);
-            g01 = f2_fma(f2_pack(cc.x, cc.y), dyy, g01);
-            g23 = f2_fma(f2_pack(cc.z, cc.w), dyy, g23);
-            const f32x2 e01 = f2_mul(g01, p01[i]), e23 = f2_mul(g23, p23[i]);
-            dA01 = f2_fma(e01, dd, dA01);
-            dA23 = f2_fma(e23, dd, dA23);
-            float lo, hi;
-            f2_unpack(f2_fma(g23, b23, f2_mul(g01, b01)), lo, hi);
-            v[2 * i] = lo + hi;
-            f2_unpack(f2_fma(e23, A23, f2_mul(e01, A01)), lo, hi);
-            v[2 * i + 1] = lo + hi;
+            const QuadBC<BF16> q = load_bc(&s_bc[(tb + i) * L + lane]);
+            f32x2 b01, b23, c01, c23, dB01 = 0ull, dB23 = 0ull, dC01 = 0ull, dC23 = 0ull;
+            QuadBC<BF16>::get(q.b, b01, b23);
+            QuadBC<BF16>::get(q.c, c01, c23);
+#pragma unroll
+            for (int k = 0; k < KC; ++k) {
+                const int x = (tb + i) * YS + chl + k * Tile::kStep;
+                const float d = s_delta[x];
+                const f32x2 dd = f2_splat(d), du = f2_splat(d * s_u[x]), dy = f2_splat(s_dy[x]);
+                const f32x2 hh01 = f2_fma(du, b01, p01[i][k]), hh23 = f2_fma(du, b23, p23[i][k]);
+                g01[k] = f2_fma(c01, dy, g01[k]);
+                g23[k] = f2_fma(c23, dy, g23[k]);
+                const f32x2 e01 = f2_mul(g01[k], p01[i][k]), e23 = f2_mul(g23[k], p23[i][k]);
+                dA01[k] = f2_fma(e01, dd, dA01[k]);
+                dA23[k] = f2_fma(e23, dd, dA23[k]);
+                float lo, hi;
+                f2_unpack(f2_fma(g23[k], b23, f2_mul(g01[k], b01)), lo, hi);
+                v[k][NV * i] = lo + hi;
+                f2_unpack(f2_fma(e23, f2_pack(A2[k][2], A2[k][3]), f2_mul(e01, f2_pack(A2[k][0], A2[k][1]))), lo, hi);
+                v[k][NV * i + 1] = lo + hi;
+                f2_unpack(f2_fma(hh23, c23, f2_mul(hh01, c01)), lo, hi);
+                v[k][NV * i + 2] = lo + hi;
+                if constexpr (NV == 4) v[k][NV * i + 3] = 0.f;
+                dB01 = f2_fma(g01[k], du, dB01);
+                dB23 = f2_fma(g23[k], du, dB23);
+                dC01 = f2_fma(hh01, dy, dC01);
+                dC23 = f2_fma(hh23, dy, dC23);
+                g01[k] = f2_mul(a01[i][k], g01[k]);
+                g23[k] = f2_mul(a23[i][k], g23[k]);
+            }
             const int w = 8 * (i % TB);
-            f2_unpack(f2_mul(g01, du), bc[w], bc[w + 1]);
-            f2_unpack(f2_mul(g23, du), bc[w + 2], bc[w + 3]);
-            f2_unpack(f2_mul(f2_fma(du, b01, p01[i]), dyy), bc[w + 4], bc[w + 5]);
-            f2_unpack(f2_mul(f2_fma(du, b23, p23[i]), dyy), bc[w + 6], bc[w + 7]);
-            g01 = f2_mul(a01[i], g01);
-            g23 = f2_mul(a23[i], g23);
+            f2_unpack(dB01, bc[w], bc[w + 1]);
+            f2_unpack(dB23, bc[w + 2], bc[w + 3]);
+            f2_unpack(dC01, bc[w + 4], bc[w + 5]);
+            f2_unpack(dC23, bc[w + 6], bc[w + 7]);
             if (i % TB == 0) {
                 const int k = chl % KW;
                 transposed_sums<8 * TB, KW, L>(bc, k);
-                const int at = k * VPL;   // token at / 8 of the TB, value at % 8: dB (below 4) or dC of this lane's states
-                float *dst = red + (i + at / 8) * (8 * L) + ((at % 8) / 4) * (4 * L) + m0 + at % 4;
+                const int o = k * VPL;   // token o / 8 of the TB, value o % 8: dB (below 4) or dC of this lane's states
+                float *dst = red + (i + o / 8) * (8 * L) + ((o % 8) / 4) * (4 * L) + m0 + o % 4;
 #pragma unroll
                 for (int x = 0; x < VPL; ++x) dst[x] = bc[x];
             }
         }
-        // du and ddt in the place of u and delta: the lanes of a channel are in one warp and have read
-        // both for these tokens
-        transposed_sums<2 * kBack, L, 1>(v, lane);
-        __syncwarp();
-        auto finish = [&](int t, float dbu, float ddA) {
-            const int at = t * YS + chl;
-            const float d = s_delta[at], u = s_u[at], dy = s_dy[at];
-            const float ddt = fmaf(u, dbu, 0.6931471805599453f * ddA) * -expm1f(-d);   // sigmoid(x) = 1 - exp(-softplus(x))
-            s_u[at] = fmaf(d, dbu, skip * dy);
-            s_delta[at] = ddt;
-            dskip = fmaf(dy, u, dskip);
-            dbias += ddt;
-        };
-        if constexpr (L <= kBack) {
+        // du, ddt and the output in the place of u, delta and dy: the lanes of a channel are in one warp and
+        // have read all three for these tokens
 #pragma unroll
-            for (int k = 0; k < kBack / L; ++k) finish(tb + lane * (kBack / L) + k, v[2 * k], v[2 * k + 1]);
-        } else {   // L = 16: one value a lane, a pair of lanes per token
-            const float other = __shfl_xor_sync(0xffffffffu, v[0], 1);
-            if ((lane & 1) == 0) finish(tb + lane / 2, v[0], other);
+        for (int k = 0; k < KC; ++k) transposed_sums<NV * kBack, L, 1>(v[k], lane);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+            auto finish = [&](int t, float dbu, float ddA, float y) {
+                const int x = t * YS + chl + k * Tile::kStep;
+                const float d = s_delta[x], u = s_u[x], dy = s_dy[x];
+                const float ddt = fmaf(u, dbu, 0.6931471805599453f * ddA) * one_minus_exp_neg(d);   // sigmoid(x) = 1 - exp(-softplus(x))
+                s_u[x] = fmaf(d, dbu, skip[k] * dy);
+                s_delta[x] = ddt;
+                s_dy[x] = fmaf(skip[k], u, y);
+                dskip[k] = fmaf(dy, u, dskip[k]);
+                dbias[k] += ddt;
+            };
+            if constexpr (L <= kBack) {
+#pragma unroll
+                for (int i = 0; i < kBack / L; ++i) finish(tb + lane * (kBack / L) + i, v[k][3 * i], v[k][3 * i + 1], v[k][3 * i + 2]);
+            } else {   // 16 lanes: two values a lane, a pair of lanes a token
+                const float y = __shfl_xor_sync(0xffffffffu, v[k][0], 1);
+                if ((lane & 1) == 0) finish(tb + lane / 2, v[k][0], v[k][1], y);
+            }
         }
         __syncthreads();
         // the block's dB and dC of these tokens (the other buffer takes the next ones meanwhile)
-        const float *all = s_red + (sb & 1) * ((kScanThreads / 32) * kBack * 8 * L);
-        for (int i = tid; i < kBack * 8 * L; i += kScanThreads) {
+        const float *all = s_red + (sb & 1) * (kScanThreads / 32 * RED);
+        for (int i = tid; i < RED; i += kScanThreads) {
             const int t = tb + i / (8 * L), x = i % (8 * L), m = x % (4 * L);
-            if (t0 + t < t1 && m < p.n) {
+            if (at.t0 + t < at.t1 && m < p.n) {
                 float s = all[i];
 #pragma unroll
-                for (int w = 1; w < kScanThreads / 32; ++w) s += all[w * (kBack * 8 * L) + i];
-                p.pBC[((int64_t)cb * p.total_tokens + t0 + t) * (2 * p.n) + (x / (4 * L)) * p.n + m] = s;
+                for (int w = 1; w < kScanThreads / 32; ++w) s += all[w * RED + i];
+                p.pBC[((int64_t)cb * p.total_tokens + at.t0 + t) * (2 * p.n) + (x / (4 * L)) * p.n + m] = s;
             }
         }
     }
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-        const int64_t tt = t0 + k * TT + srow;
-        if (tt < t1 && left > 0) {
-            float o[E];
-            const int at = (k * TT + srow) * YS + scol;
-#pragma unroll
-            for (int i = 0; i < E; ++i) o[i] = s_u[at + i];
-            store_piece<BF16, E>(p.du, tt * p.D + sc, left, p.vec, o);
-#pragma unroll
-            for (int i = 0; i < E; ++i) o[i] = s_delta[at + i];
-            store_piece<BF16, E>(p.ddt, tt * p.D + sc, left, p.vec, o);
+#pragma unroll 2
+    for (int i = 0; i < Tile::kR; ++i) {
+        const int on = at.on(i), x = at.row(i) * YS + at.col();
+        const int64_t off = at.off(i, p.D);
+        const float2 du = *reinterpret_cast<const float2 *>(&s_u[x]), ddt = *reinterpret_cast<const float2 *>(&s_delta[x]);
+        Pair<BF16>::store(p.du, off, on, p.vec, du.x, du.y);
+        Pair<BF16>::store(p.ddt, off, on, p.vec, ddt.x, ddt.y);
+        if (p.z) {
+            Pair<BF16> rz, rdo;
+            rz.load(p.z, off, on, p.vec);
+            rdo.load(p.dout, off, on, p.vec);
+            const float2 y = *reinterpret_cast<const float2 *>(&s_dy[x]), z = rz.get(p.vec), o = rdo.get(p.vec);
+            const float s0 = sigmoid_fast(z.x), s1 = sigmoid_fast(z.y);
+            Pair<BF16>::store(p.dz, off, on, p.vec, o.x * y.x * s0 * fmaf(z.x, 1.f - s0, 1.f),
+                             o.y * y.y * s1 * fmaf(z.y, 1.f - s1, 1.f));
         }
     }
 #pragma unroll
-    for (int w = L / 2; w > 0; w >>= 1) {
-        dskip += __shfl_xor_sync(0xffffffffu, dskip, w);
-        dbias += __shfl_xor_sync(0xffffffffu, dbias, w);
-    }
-    if (active) {
-        float e[4];
-        f2_unpack(dA01, e[0], e[1]);
-        f2_unpack(dA23, e[2], e[3]);
-        store_quad(p.H + row, m0, p.n, p.vecn, e);   // read above by this thread
-        if (lane == 0) {
-            p.pskip[rec * p.D + c] = dskip;
-            p.pbias[rec * p.D + c] = dbias;
+    for (int k = 0; k < KC; ++k) {
+#pragma unroll
+        for (int w = L / 2; w > 0; w >>= 1) {
+            dskip[k] += __shfl_xor_sync(0xffffffffu, dskip[k], w);
+            dbias[k] += __shfl_xor_sync(0xffffffffu, dbias[k], w);
+        }
+        if (chl + k * Tile::kStep < at.left) {
+            const int64_t c = at.c0 + chl + k * Tile::kStep;
+            float e[4];
+            f2_unpack(dA01[k], e[0], e[1]);
+            f2_unpack(dA23[k], e[2], e[3]);
+            store_quad(p.H + (rec * p.D + c) * p.n, m0, p.n, p.vecn, e);   // read above by this thread
+            if (lane == 0) {
+                p.pskip[rec * p.D + c] = dskip[k];
+                p.pbias[rec * p.D + c] = dbias[k];
+            }
         }
     }
 }
