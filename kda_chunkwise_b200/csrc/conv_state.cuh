@@ -59,14 +59,28 @@ struct ChannelGroup {
     }
 };
 
+// The taps of a thread's channels: W floats of a channel lie together, so that four taps are one load.
 template <int W, int E, class Group>
 __device__ __forceinline__ void load_taps(const ConvStateParams &p, const Group &cg, float (&w)[W][E], float (&bias)[E]) {
+    const bool whole = (reinterpret_cast<uintptr_t>(p.w) & (W * 4 - 1)) == 0;   // (a power of two where it matters)
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         const int64_t c = cg.c0 + i * cg.step;
-        bias[i] = i < cg.count && p.bias ? p.bias[c] : 0.f;
+        const bool on = i < cg.count;
+        bias[i] = on && p.bias ? __ldg(p.bias + c) : 0.f;
+        uint32_t r[W];
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = i < cg.count ? p.w[c * W + j] : 0.f;
+        for (int j = 0; j < W; ++j) r[j] = 0u;
+        if constexpr (W == 2 || W == 4) {
+            if (whole) {
+                load_if<W * 4, true>(p.w + c * W, on, r);
+#pragma unroll
+                for (int j = 0; j < W; ++j) w[j][i] = __uint_as_float(r[j]);
+                continue;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][i] = on ? __ldg(p.w + c * W + j) : 0.f;
     }
 }
 

@@ -1279,6 +1279,12 @@ kda_status with_lanes(int n, F f) {
     }
 }
 
+// f(integral_constant<bool, b>)
+template <class F>
+kda_status with_flag(bool b, F f) {
+    return b ? f(std::integral_constant<bool, true>()) : f(std::integral_constant<bool, false>());
+}
+
 // f(integral_constant<bool, bf16>)
 template <class F>
 kda_status with_dtype(kda_dtype t, F f) {
@@ -1288,7 +1294,7 @@ kda_status with_dtype(kda_dtype t, F f) {
 // channels of a block of scanning threads that take KC channels each, and such blocks of a group
 int scan_channels(int n, int KC) { return KC * (kda::kScanThreads / scan_lanes(n)); }
 int scan_blocks_of_group(int D, int n, int G, int KC) { return (D / G + scan_channels(n, KC) - 1) / scan_channels(n, KC); }
-int scan_bwd_chunk(int n) { const int L = scan_lanes(n); return L >= 4 ? 64 : 16 * L; }   // ScanBwdTile::kTC
+int scan_bwd_chunk(int n) { const int L = scan_lanes(n); return L > 4 ? 64 : (L == 4 ? 32 : 16 * L); }   // ScanBwdTile::kTC
 
 bool scan_sizes_ok(int64_t rows, int32_t seqs, int32_t D, int32_t n, int32_t G) {
     return rows >= 0 && rows <= 0x7fffffffLL && seqs >= 0 && D > 0 && n > 0 && G > 0 && D % G == 0;
@@ -1451,20 +1457,24 @@ kda_status kda_selective_scan_step(const void *u, const void *dt, const float *A
     p.state = state;
     p.out = out;
     p.N = N; p.D = D; p.n = n; p.G = G;
-    p.vecn = n % 4 == 0 && all_aligned({B, C, state});
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return with_dtype(dtype, [&](auto bf16) {
         return with_lanes(n, [&](auto lanes) {
             constexpr bool kBf16 = decltype(bf16)::value;
             constexpr int L = decltype(lanes)::value;
             const int64_t bx = ((int64_t)D * L + kda::kScanStepThreads - 1) / kda::kScanStepThreads;
-            if (N >= 8) {
-                const dim3 grid((unsigned)bx, (unsigned)std::min<int64_t>((N + 3) / 4, 65535));
-                kda::scan_step_kernel<kBf16, L, 4><<<grid, kda::kScanStepThreads, 0, s>>>(p);
-            } else {
-                kda::scan_step_kernel<kBf16, L, 1><<<dim3((unsigned)bx, (unsigned)N), kda::kScanStepThreads, 0, s>>>(p);
-            }
-            return launched("selective_scan_step launch");
+            return with_flag(n % 4 == 0 && all_aligned({B, C, state}), [&](auto v) {
+                constexpr bool VEC = decltype(v)::value;
+                // two rows a thread once every SM has several blocks
+                if (bx * N >= 16 * (int64_t)device_sm_count()) {
+                    const dim3 grid((unsigned)bx, (unsigned)std::min<int64_t>((N + 1) / 2, 65535));
+                    kda::scan_step_kernel<kBf16, L, 2, VEC><<<grid, kda::kScanStepThreads, 0, s>>>(p);
+                } else {
+                    const dim3 grid((unsigned)bx, (unsigned)std::min<int32_t>(N, 65535));
+                    kda::scan_step_kernel<kBf16, L, 1, VEC><<<grid, kda::kScanStepThreads, 0, s>>>(p);
+                }
+                return launched("selective_scan_step launch");
+            });
         });
     });
 }
@@ -1544,9 +1554,10 @@ kda_status kda_selective_scan_bwd(const void *u, const void *dt, const float *A_
     p.num_seqs = num_seqs;
     p.D = D; p.n = n; p.G = G;
     p.cbg = scan_blocks_of_group(D, n, G, kda::kBackKC);
-    p.vec = (D / G) % 2 == 0 && all_aligned({u, dt, z, dout, du, ddt, dz});
+    const bool vec = (D / G) % 4 == 0 && all_aligned({u, dt, z, dout, du, ddt, dz});
     p.vecn = n % 4 == 0 && all_aligned({B, C, initial_state, dfinal_state, dinitial_state});
-    const int64_t blocks = space.records * G * p.cbg, bc_blocks = (total_tokens * G * 2 * n + 255) / 256;
+    const int64_t blocks = space.records * G * p.cbg, bc_each = n % 2 == 0 ? 4 : 1;
+    const int64_t bc_blocks = (total_tokens * G * 2 * n / bc_each + 255) / 256;
     const int64_t w_blocks = ((int64_t)D * (n + 2) + 31) / 32;
     if (blocks > 0x7fffffffLL || bc_blocks > 0x7fffffffLL || w_blocks > 0x7fffffffLL)
         return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_bwd: too many tokens, sequences and channels");
@@ -1555,24 +1566,28 @@ kda_status kda_selective_scan_bwd(const void *u, const void *dt, const float *A_
             constexpr bool kBf16 = decltype(bf16)::value;
             constexpr int L = decltype(lanes)::value;
             using SM = kda::ScanBwdSmem<kBf16, L>;
-            cudaError_t e = cudaFuncSetAttribute(kda::scan_bwd_chunk_kernel<kBf16, L>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kChunk);
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(kda::scan_bwd_grad_kernel<kBf16, L>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kGrad);
-            if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(selective_scan_bwd)");
-            kda::scan_bwd_chunk_kernel<kBf16, L><<<(unsigned)blocks, kda::kScanThreads, SM::kChunk, s>>>(p);
-            const int64_t quads = (int64_t)D * L;
-            const dim3 chain((unsigned)((quads + kda::kChainThreads - 1) / kda::kChainThreads),
-                             (unsigned)std::min<int32_t>(num_seqs, 65535), 2);
-            kda::scan_bwd_chain_kernel<L><<<chain, kda::kChainThreads, 0, s>>>(p);
-            kda::scan_bwd_grad_kernel<kBf16, L><<<(unsigned)blocks, kda::kScanThreads, SM::kGrad, s>>>(p);
-            if (bc_blocks > 0) kda::scan_bwd_bc_kernel<kBf16><<<(unsigned)bc_blocks, 256, 0, s>>>(p);
-            kda::scan_bwd_weights_kernel<<<(unsigned)w_blocks, dim3(32, kda::kColRows), 0, s>>>(p);
-            return launched("selective_scan_bwd launch", bc_blocks > 0 ? 5 : 4);
+            return with_flag(vec, [&](auto v) {
+                constexpr bool VEC = decltype(v)::value;
+                cudaError_t e = cudaFuncSetAttribute(kda::scan_bwd_chunk_kernel<kBf16, L, VEC>,
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kChunk);
+                if (e == cudaSuccess)
+                    e = cudaFuncSetAttribute(kda::scan_bwd_grad_kernel<kBf16, L, VEC>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kGrad);
+                if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(selective_scan_bwd)");
+                kda::scan_bwd_chunk_kernel<kBf16, L, VEC><<<(unsigned)blocks, kda::kScanThreads, SM::kChunk, s>>>(p);
+                const int64_t quads = (int64_t)D * L;
+                const dim3 chain((unsigned)((quads + kda::kChainThreads - 1) / kda::kChainThreads),
+                                 (unsigned)std::min<int32_t>(num_seqs, 65535), 2);
+                kda::scan_bwd_chain_kernel<L><<<chain, kda::kChainThreads, 0, s>>>(p);
+                kda::scan_bwd_grad_kernel<kBf16, L, VEC><<<(unsigned)blocks, kda::kScanThreads, SM::kGrad, s>>>(p);
+                if (bc_blocks > 0 && bc_each == 4) kda::scan_bwd_bc_kernel<kBf16, 4><<<(unsigned)bc_blocks, 256, 0, s>>>(p);
+                else if (bc_blocks > 0) kda::scan_bwd_bc_kernel<kBf16, 1><<<(unsigned)bc_blocks, 256, 0, s>>>(p);
+                kda::scan_bwd_weights_kernel<<<(unsigned)w_blocks, dim3(32, kda::kColRows), 0, s>>>(p);
+                return launched("selective_scan_bwd launch", bc_blocks > 0 ? 5 : 4);
+            });
         });
     });
 }
-
 namespace {
 
 constexpr int kConvFwdElems16 = 8, kConvFwdElems32 = 4, kConvBwdElems = 4;
@@ -1605,12 +1620,6 @@ kda_status conv_check(const char *where, int64_t rows, int32_t seqs, int32_t H, 
     if (width < 1 || width > kda::kConvMaxWidth) return fail(KDA_ERR_INVALID_ARG, w + ": width must be in [1, 4]");
     if (!known_dtype(dtype)) return fail(KDA_ERR_INVALID_ARG, w + ": dtype must be KDA_DTYPE_BF16 or KDA_DTYPE_F32");
     return KDA_OK;
-}
-
-// f(integral_constant<bool, b>)
-template <class F>
-kda_status with_flag(bool b, F f) {
-    return b ? f(std::integral_constant<bool, true>()) : f(std::integral_constant<bool, false>());
 }
 
 // f(integral_constant<int, W>)

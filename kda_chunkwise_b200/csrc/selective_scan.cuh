@@ -503,15 +503,14 @@ struct ScanStepParams {
     float *state;                         // [N, D, n], in place
     void *out;                            // [N, D]
     int N, D, n, G;
-    bool vecn;
 };
 
 constexpr int kScanStepThreads = 256;
 
 // One token of N states: the state is read once and written once (0.9 flop a byte), so the kernel
-// streams it.  A thread owns four states of one channel (16 bytes), in U rows of the batch at once so
-// that enough loads are in flight; the decay's weights are read once for the U rows.
-template <bool BF16, int L, int U>
+// streams it.  A thread owns four states of one channel (16 bytes) in U rows of the batch at once, so
+// that enough loads are in flight; the decay's weights are read once for all its rows.
+template <bool BF16, int L, int U, bool VEC>
 __global__ void __launch_bounds__(kScanStepThreads) scan_step_kernel(const ScanStepParams p) {
     const int64_t q = (int64_t)blockIdx.x * kScanStepThreads + threadIdx.x;   // quad of a row of the batch
     const int lane = static_cast<int>(q % L), m0 = 4 * lane;
@@ -524,61 +523,45 @@ __global__ void __launch_bounds__(kScanStepThreads) scan_step_kernel(const ScanS
     int v4 = p.n - m0;
     v4 = active && v4 > 0 ? (v4 > 4 ? 4 : v4) : 0;
     for (int64_t r0 = (int64_t)blockIdx.y * U; r0 < p.N; r0 += (int64_t)gridDim.y * U) {
-        float h[U][4], u[U], dt[U], z[U];
-        Quad<BF16> B[U], C[U];
+        Piece<false, 4> rh[U];
+        Piece<BF16, 4> rB[U], rC[U];
+        Piece<BF16, 1> ru[U], rdt[U], rz[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            const int64_t r = r0 + k;
-            const bool on = active && r < p.N;
-            h[k][0] = h[k][1] = h[k][2] = h[k][3] = 0.f;
-            if (on) {
-                if (p.vecn) {
-                    if (m0 < p.n) {
-                        const float4 x = __ldcs(reinterpret_cast<const float4 *>(p.state + (r * p.D + c) * p.n + m0));
-                        h[k][0] = x.x; h[k][1] = x.y; h[k][2] = x.z; h[k][3] = x.w;
-                    }
-                } else {
-                    load_quad(p.state + (r * p.D + c) * p.n, m0, p.n, false, h[k]);
-                }
-            }
-            u[k] = on ? load_elem<BF16>(p.u, r * p.D + c) : 0.f;
-            dt[k] = on ? load_elem<BF16>(p.dt, r * p.D + c) : 0.f;
-            z[k] = on && p.z ? load_elem<BF16>(p.z, r * p.D + c) : 0.f;
-            B[k].load(p.B, (r * p.G + g) * p.n + m0, on ? v4 : 0, p.vecn);
-            C[k].load(p.C, (r * p.G + g) * p.n + m0, on ? v4 : 0, p.vecn);
+            const int64_t r = r0 + k, x = r * p.D + c;
+            const bool in = r < p.N, on = active && in;
+            load_piece<false, 4, VEC, false>(p.state, x * p.n + m0, in ? v4 : 0, rh[k]);
+            load_piece<BF16, 1, false>(p.u, x, on, ru[k]);
+            load_piece<BF16, 1, false>(p.dt, x, on, rdt[k]);
+            load_piece<BF16, 1, false>(p.z, x, on && p.z, rz[k]);
+            load_piece<BF16, 4, VEC>(p.B, (r * p.G + g) * p.n + m0, in ? v4 : 0, rB[k]);
+            load_piece<BF16, 4, VEC>(p.C, (r * p.G + g) * p.n + m0, in ? v4 : 0, rC[k]);
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            const int64_t r = r0 + k;
-            const bool on = active && r < p.N;
-            const float d = softplus(dt[k] + bias), du = d * u[k];
-            float b[4], cc[4], y = 0.f;
-            f32x2 lo, hi;
-            QuadBC<BF16>::get(B[k].get(p.vecn), lo, hi);
-            f2_unpack(lo, b[0], b[1]);
-            f2_unpack(hi, b[2], b[3]);
-            QuadBC<BF16>::get(C[k].get(p.vecn), lo, hi);
-            f2_unpack(lo, cc[0], cc[1]);
-            f2_unpack(hi, cc[2], cc[3]);
+            const int64_t r = r0 + k, x = r * p.D + c;
+            float h[4], b[4], cc[4], u[1], dt[1], y = 0.f;
+            piece_to_f32<false, 4, VEC>(rh[k], h);
+            piece_to_f32<BF16, 4, VEC>(rB[k], b);
+            piece_to_f32<BF16, 4, VEC>(rC[k], cc);
+            piece_to_f32<BF16, 1, false>(ru[k], u);
+            piece_to_f32<BF16, 1, false>(rdt[k], dt);
+            const float d = softplus(dt[0] + bias), du = d * u[0];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                h[k][i] = fmaf(ex2_approx(A2[i] * d), h[k][i], du * b[i]);
-                y = fmaf(h[k][i], cc[i], y);
+                h[i] = fmaf(ex2_approx(A2[i] * d), h[i], du * b[i]);
+                y = fmaf(h[i], cc[i], y);
             }
 #pragma unroll
             for (int w = L / 2; w > 0; w >>= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
-            if (!on) continue;
-            if (p.vecn) {
-                if (m0 < p.n)
-                    __stcs(reinterpret_cast<float4 *>(p.state + (r * p.D + c) * p.n + m0),
-                           make_float4(h[k][0], h[k][1], h[k][2], h[k][3]));
-            } else {
-                store_quad(p.state + (r * p.D + c) * p.n, m0, p.n, false, h[k]);
-            }
-            if (lane == 0) {
-                y = fmaf(skip, u[k], y);
-                if (p.z) y *= silu(z[k]);
-                store_out(p.out, r * p.D + c, !BF16, y);
+            if (r >= p.N) break;
+            store_piece<false, 4, VEC>(p.state, x * p.n + m0, v4, h);
+            if (lane == 0 && active) {
+                float z[1];
+                piece_to_f32<BF16, 1, false>(rz[k], z);
+                y = fmaf(skip, u[0], y);
+                if (p.z) y *= silu(z[0]);
+                store_out(p.out, x, !BF16, y);
             }
         }
     }

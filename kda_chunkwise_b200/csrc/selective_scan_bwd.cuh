@@ -14,8 +14,8 @@
 //                             start, in one pass (the running product of decays takes no exponential)
 //   2. scan_bwd_chain_kernel  the states at the chunk starts (forwards) and the gradients at the chunk
 //                             ends (backwards), in place
-//   3. scan_bwd_grad_kernel   every chunk's gradients: a pass forwards that keeps every eighth state,
-//                             then eight tokens at a time recomputed into registers and run backwards;
+//   3. scan_bwd_grad_kernel   every chunk's gradients: a pass forwards that keeps every kBack-th state,
+//                             then kBack tokens at a time recomputed into registers and run backwards;
 //                             du, ddt and the output take the places of u, delta and dy
 //   4. two sums of partial results over channel blocks (dB, dC) and over chunks (the weights)
 // Under three exponentials per (token, channel, state); sums are taken in a fixed order, so results do not
@@ -41,44 +41,44 @@ struct ScanBwdParams {
     float *pBC;     // [channel blocks, T, 2 n] the block's share of dB, dC
     int64_t total_tokens, records;
     int num_seqs, D, n, G, cbg;
-    bool vec, vecn;
+    bool vecn;
 };
 
 constexpr int kBackKC = 2;   // channels of a thread: B and C are read, and dB and dC summed over a warp, once for both
-constexpr int kBack = 8;     // tokens recomputed into registers at once
 
 template <int L>
 struct ScanBwdTile {
     static constexpr int kStep = kScanThreads / L;
     static constexpr int kCH = kBackKC * kStep;             // channels of a block
-    static constexpr int kTC = L >= 4 ? 64 : 16 * L;        // tokens of a chunk
-    static constexpr int kPR = kCH / 2;                     // pairs of channels of a row
-    static constexpr int kR = kTC * kPR / kScanThreads;     // pairs of a chunk per thread
-    static constexpr int kYS = kCH + 32 / L;                // row stride: the lanes' rows fall on different banks
+    static constexpr int kTC = L > 4 ? 64 : (L == 4 ? 32 : 16 * L);   // tokens of a chunk
+    static constexpr int kBack = L > 4 ? 8 : 4;             // tokens recomputed into registers at once
+    static constexpr int kFR = kCH / 4;                     // fours of channels of a row
+    static constexpr int kR = kTC * kFR / kScanThreads;     // fours of a chunk per thread
+    static constexpr int kYS = kCH + (L == 16 ? 4 : 32 / L);   // row stride: the lanes' rows fall on different banks
 };
 
-// Where a block's channels lie and which of a chunk's rows and channel pairs a thread moves.
+// Where a block's channels lie and which of a chunk's rows and fours of channels a thread moves.
 template <int L>
 struct ScanBwdPlace {
     using Tile = ScanBwdTile<L>;
     int64_t t0, t1, c0;
     int left;   // channels of the group from c0 on
-    __device__ __forceinline__ int row(int i) const { return threadIdx.x / Tile::kPR + i * (kScanThreads / Tile::kPR); }
-    __device__ __forceinline__ int col() const { return 2 * (threadIdx.x % Tile::kPR); }
-    __device__ __forceinline__ int on(int i) const {   // how many channels of pair i exist
+    __device__ __forceinline__ int row(int i) const { return threadIdx.x / Tile::kFR + i * (kScanThreads / Tile::kFR); }
+    __device__ __forceinline__ int col() const { return 4 * (threadIdx.x % Tile::kFR); }
+    __device__ __forceinline__ int on(int i) const {   // how many channels of four i exist
         const int n = left - col();
-        return t0 + row(i) < t1 && n > 0 ? (n > 2 ? 2 : n) : 0;
+        return t0 + row(i) < t1 && n > 0 ? (n > 4 ? 4 : n) : 0;
     }
     __device__ __forceinline__ int64_t off(int i, int D) const { return (t0 + row(i)) * D + c0 + col(); }
 };
 
 // Stages delta, u and dy of the block's channels ([kTC][kYS] each), B and C.  Rows past the end and channels
 // past the group are zero: there a = 1 and every gradient is zero.
-template <bool BF16, int L>
+template <bool BF16, int L, bool VEC>
 __device__ __forceinline__ void stage_bwd(const ScanBwdParams &p, const ScanBwdPlace<L> &at, int g, float *s_delta, float *s_u,
                                           float *s_dy, QuadBC<BF16> *s_bc) {
     using Tile = ScanBwdTile<L>;
-    constexpr int YS = Tile::kYS, R = Tile::kR, AHEAD = R < 8 ? R : 8;
+    constexpr int YS = Tile::kYS, R = Tile::kR, AHEAD = R < 4 ? R : 4;
     for (int i = threadIdx.x; i < Tile::kTC * L; i += kScanThreads) {   // row i / L, states 4 (i % L) ..
         const int64_t tb = at.t0 + i / L;
         const int mm = 4 * (i % L);
@@ -90,34 +90,39 @@ __device__ __forceinline__ void stage_bwd(const ScanBwdParams &p, const ScanBwdP
         s_bc[i].b = rB.get(p.vecn);
         s_bc[i].c = rC.get(p.vecn);
     }
-    const float b0 = p.dt_bias && at.left > at.col() ? p.dt_bias[at.c0 + at.col()] : 0.f;
-    const float b1 = p.dt_bias && at.left > at.col() + 1 ? p.dt_bias[at.c0 + at.col() + 1] : 0.f;
+    float bias[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) bias[k] = p.dt_bias && at.left > at.col() + k ? p.dt_bias[at.c0 + at.col() + k] : 0.f;
 #pragma unroll 1
     for (int i0 = 0; i0 < R; i0 += AHEAD) {
-        Pair<BF16> ru[AHEAD], rdt[AHEAD], rdo[AHEAD], rz[AHEAD];
+        Piece<BF16, 4> ru[AHEAD], rdt[AHEAD], rdo[AHEAD], rz[AHEAD];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-            const int i = i0 + k, on = at.on(i);
-            const int64_t off = at.off(i, p.D);
-            ru[k].load(p.u, off, on, p.vec);
-            rdt[k].load(p.dt, off, on, p.vec);
-            rdo[k].load(p.dout, off, on, p.vec);
-            rz[k].load(p.z, off, p.z ? on : 0, p.vec);
+            const int on = at.on(i0 + k);
+            const int64_t off = at.off(i0 + k, p.D);
+            load_piece<BF16, 4, VEC>(p.u, off, on, ru[k]);
+            load_piece<BF16, 4, VEC>(p.dt, off, on, rdt[k]);
+            load_piece<BF16, 4, VEC>(p.dout, off, on, rdo[k]);
+            load_piece<BF16, 4, VEC>(p.z, off, p.z ? on : 0, rz[k]);
         }
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-            const int i = i0 + k, on = at.on(i), x = at.row(i) * YS + at.col();
-            const float2 dt = rdt[k].get(p.vec);
-            float2 dy = rdo[k].get(p.vec);
+            const int on = at.on(i0 + k), x = at.row(i0 + k) * YS + at.col();
+            float u[4], d[4], dy[4];
+            piece_to_f32<BF16, 4, VEC>(ru[k], u);
+            piece_to_f32<BF16, 4, VEC>(rdt[k], d);
+            piece_to_f32<BF16, 4, VEC>(rdo[k], dy);
             if (p.z) {
-                const float2 z = rz[k].get(p.vec);
-                dy.x *= silu(z.x);
-                dy.y *= silu(z.y);
+                float z[4];
+                piece_to_f32<BF16, 4, VEC>(rz[k], z);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) dy[w] *= silu(z[w]);
             }
-            *reinterpret_cast<float2 *>(&s_delta[x]) =
-                make_float2(on > 0 ? softplus(dt.x + b0) : 0.f, on > 1 ? softplus(dt.y + b1) : 0.f);
-            *reinterpret_cast<float2 *>(&s_u[x]) = ru[k].get(p.vec);
-            *reinterpret_cast<float2 *>(&s_dy[x]) = dy;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) d[w] = on > w ? softplus(d[w] + bias[w]) : 0.f;
+            *reinterpret_cast<float4 *>(&s_delta[x]) = make_float4(d[0], d[1], d[2], d[3]);
+            *reinterpret_cast<float4 *>(&s_u[x]) = make_float4(u[0], u[1], u[2], u[3]);
+            *reinterpret_cast<float4 *>(&s_dy[x]) = make_float4(dy[0], dy[1], dy[2], dy[3]);
         }
     }
 }
@@ -128,13 +133,13 @@ struct ScanBwdSmem {
     static constexpr int kAct = Tile::kTC * Tile::kYS * 4;                               // delta, u, dy
     static constexpr int kBC = Tile::kTC * L * (int)sizeof(QuadBC<BF16>);
     static constexpr int kChunk = 3 * kAct + kBC;                                        // of the chunk kernel
-    static constexpr int kCkpt = Tile::kTC / kBack * kBackKC * 16 * kScanThreads;        // every eighth state
-    static constexpr int kRed = 2 * (kScanThreads / 32) * kBack * 8 * L * 4;             // two buffers of the warps' dB, dC rows
+    static constexpr int kCkpt = Tile::kTC / Tile::kBack * kBackKC * 16 * kScanThreads;  // every kBack-th state
+    static constexpr int kRed = 2 * (kScanThreads / 32) * Tile::kBack * 8 * L * 4;             // two buffers of the warps' dB, dC rows
     static constexpr int kGrad = kChunk + kCkpt + kRed;
 };
 
-template <bool BF16, int L>
-__global__ void __launch_bounds__(kScanThreads) scan_bwd_chunk_kernel(const ScanBwdParams p) {
+template <bool BF16, int L, bool VEC>
+__global__ void __launch_bounds__(kScanThreads, L > 4 ? 3 : 5) scan_bwd_chunk_kernel(const ScanBwdParams p) {
     using Tile = ScanBwdTile<L>;
     using SM = ScanBwdSmem<BF16, L>;
     constexpr int CH = Tile::kCH, YS = Tile::kYS, KC = kBackKC;
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_bwd_chunk_kernel(const Scan
         P01[k] = P23[k] = f2_splat(1.f);
         sum_delta[k] = 0.f;
     }
-    stage_bwd<BF16, L>(p, at, g, s_delta, s_u, s_dy, s_bc);
+    stage_bwd<BF16, L, VEC>(p, at, g, s_delta, s_u, s_dy, s_bc);
     __syncthreads();
     const int steps = static_cast<int>(at.t1 - at.t0);
 #pragma unroll 4
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_bwd_chunk_kernel(const Scan
 }
 
 constexpr int kChainThreads = 128;
-constexpr int kChainAhead = 8;   // records in flight
+constexpr int kChainAhead = 16;   // records in flight
 
 // grid: x = quads of [D, 4 L] in blocks of kChainThreads, y = sequence, z = direction (0: states forwards,
 // 1: gradients backwards).  Every record's value is replaced by what comes into the chunk.
@@ -228,35 +233,39 @@ __global__ void __launch_bounds__(kChainThreads) scan_bwd_chain_kernel(const Sca
         float cur[4] = {0.f, 0.f, 0.f, 0.f};
         const float *init = back ? p.dhN : p.h0;
         if (init) load_quad(init + (seq * p.D + c) * p.n, m0, p.n, p.vecn, cur);
-        for (int64_t i0 = 0; i0 < count; i0 += kChainAhead) {
+        auto record = [&](int64_t i) { return base + (back ? count - 1 - i : i); };
+        auto pass = [&](int64_t r, const float (&x)[4], float sd) {   // what comes in replaces the record; what goes out
+            store_quad(X + (r * p.D + c) * p.n, m0, p.n, p.vecn, cur);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) cur[w] = fmaf(ex2_approx(A2[w] * sd), cur[w], x[w]);
+        };
+        int64_t i = 0;
+        for (; i + kChainAhead <= count; i += kChainAhead) {
             float x[kChainAhead][4], sd[kChainAhead];
 #pragma unroll
             for (int k = 0; k < kChainAhead; ++k) {
-                const int64_t i = i0 + k;
-                if (i >= count) break;
-                const int64_t r = base + (back ? count - 1 - i : i);
+                const int64_t r = record(i + k);
                 load_quad(X + (r * p.D + c) * p.n, m0, p.n, p.vecn, x[k]);
                 sd[k] = p.sum_delta[r * p.D + c];
             }
 #pragma unroll
-            for (int k = 0; k < kChainAhead; ++k) {
-                const int64_t i = i0 + k;
-                if (i >= count) break;
-                const int64_t r = base + (back ? count - 1 - i : i);
-                store_quad(X + (r * p.D + c) * p.n, m0, p.n, p.vecn, cur);
-#pragma unroll
-                for (int w = 0; w < 4; ++w) cur[w] = fmaf(ex2_approx(A2[w] * sd[k]), cur[w], x[k][w]);
-            }
+            for (int k = 0; k < kChainAhead; ++k) pass(record(i + k), x[k], sd[k]);
+        }
+        for (; i < count; ++i) {
+            const int64_t r = record(i);
+            float x[4];
+            load_quad(X + (r * p.D + c) * p.n, m0, p.n, p.vecn, x);
+            pass(r, x, p.sum_delta[r * p.D + c]);
         }
         if (back && p.dh0) store_quad(p.dh0 + (seq * p.D + c) * p.n, m0, p.n, p.vecn, cur);
     }
 }
 
-template <bool BF16, int L>
-__global__ void __launch_bounds__(kScanThreads) scan_bwd_grad_kernel(const ScanBwdParams p) {
+template <bool BF16, int L, bool VEC>
+__global__ void __launch_bounds__(kScanThreads, L > 4 ? 2 : 3) scan_bwd_grad_kernel(const ScanBwdParams p) {
     using Tile = ScanBwdTile<L>;
     using SM = ScanBwdSmem<BF16, L>;
-    constexpr int TC = Tile::kTC, CH = Tile::kCH, YS = Tile::kYS, KC = kBackKC;
+    constexpr int TC = Tile::kTC, CH = Tile::kCH, YS = Tile::kYS, KC = kBackKC, kBack = Tile::kBack;
     constexpr int KW = 32 / L;               // channels side by side in a warp
     constexpr int TB = KW > 8 ? KW / 8 : 1;  // tokens whose dB, dC rows are summed over the warp at once
     constexpr int VPL = 8 * TB / KW;         // values of them a lane is left with
@@ -308,7 +317,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_bwd_grad_kernel(const ScanB
         dskip[k] = dbias[k] = 0.f;
     }
     if (!chunk) return;
-    stage_bwd<BF16, L>(p, at, g, s_delta, s_u, s_dy, s_bc);
+    stage_bwd<BF16, L, VEC>(p, at, g, s_delta, s_u, s_dy, s_bc);
     __syncthreads();
 
     // forwards: the state before every kBack tokens (read back by the thread that wrote it)
@@ -341,6 +350,8 @@ __global__ void __launch_bounds__(kScanThreads) scan_bwd_grad_kernel(const ScanB
     }
 
     // backwards
+    const int tokens = static_cast<int>(at.t1 - at.t0);
+    float *bc_out = p.pBC + ((int64_t)cb * p.total_tokens + at.t0) * (2 * p.n);
 #pragma unroll 1
     for (int sb = blocks - 1; sb >= 0; --sb) {
         const int tb = sb * kBack;
@@ -369,7 +380,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_bwd_grad_kernel(const ScanB
         }
         float *red = s_red + (sb & 1) * (kScanThreads / 32 * RED) + warp * RED;
         // sums over a channel's states: of g B (the gradient of delta u), of e A (of delta), and the output
-        constexpr int NV = L > kBack ? 4 : 3;   // (16 lanes: four a token, so that two lanes hold one)
+        constexpr int NV = L > kBack ? 4 : 3;   // (more lanes than tokens: four a token, so that two lanes hold one)
         float v[KC][NV * kBack];
         float bc[8 * TB];
 #pragma unroll
@@ -446,13 +457,14 @@ __global__ void __launch_bounds__(kScanThreads) scan_bwd_grad_kernel(const ScanB
         __syncthreads();
         // the block's dB and dC of these tokens (the other buffer takes the next ones meanwhile)
         const float *all = s_red + (sb & 1) * (kScanThreads / 32 * RED);
-        for (int i = tid; i < RED; i += kScanThreads) {
-            const int t = tb + i / (8 * L), x = i % (8 * L), m = x % (4 * L);
-            if (at.t0 + t < at.t1 && m < p.n) {
+#pragma unroll
+        for (int i0 = 0; i0 < RED; i0 += kScanThreads) {
+            const int i = i0 + tid, t = tb + i / (8 * L), x = i % (8 * L), m = x % (4 * L);
+            if (i < RED && t < tokens && m < p.n) {
                 float s = all[i];
 #pragma unroll
                 for (int w = 1; w < kScanThreads / 32; ++w) s += all[w * RED + i];
-                p.pBC[((int64_t)cb * p.total_tokens + at.t0 + t) * (2 * p.n) + (x / (4 * L)) * p.n + m] = s;
+                bc_out[t * (2 * p.n) + (x / (4 * L)) * p.n + m] = s;
             }
         }
     }
@@ -460,17 +472,25 @@ __global__ void __launch_bounds__(kScanThreads) scan_bwd_grad_kernel(const ScanB
     for (int i = 0; i < Tile::kR; ++i) {
         const int on = at.on(i), x = at.row(i) * YS + at.col();
         const int64_t off = at.off(i, p.D);
-        const float2 du = *reinterpret_cast<const float2 *>(&s_u[x]), ddt = *reinterpret_cast<const float2 *>(&s_delta[x]);
-        Pair<BF16>::store(p.du, off, on, p.vec, du.x, du.y);
-        Pair<BF16>::store(p.ddt, off, on, p.vec, ddt.x, ddt.y);
+        Piece<BF16, 4> rz, rdo;
+        load_piece<BF16, 4, VEC>(p.z, off, p.z ? on : 0, rz);
+        load_piece<BF16, 4, VEC>(p.dout, off, p.z ? on : 0, rdo);
+        const float4 du = *reinterpret_cast<const float4 *>(&s_u[x]), ddt = *reinterpret_cast<const float4 *>(&s_delta[x]);
+        const float du4[4] = {du.x, du.y, du.z, du.w}, ddt4[4] = {ddt.x, ddt.y, ddt.z, ddt.w};
+        store_piece<BF16, 4, VEC>(p.du, off, on, du4);
+        store_piece<BF16, 4, VEC>(p.ddt, off, on, ddt4);
         if (p.z) {
-            Pair<BF16> rz, rdo;
-            rz.load(p.z, off, on, p.vec);
-            rdo.load(p.dout, off, on, p.vec);
-            const float2 y = *reinterpret_cast<const float2 *>(&s_dy[x]), z = rz.get(p.vec), o = rdo.get(p.vec);
-            const float s0 = sigmoid_fast(z.x), s1 = sigmoid_fast(z.y);
-            Pair<BF16>::store(p.dz, off, on, p.vec, o.x * y.x * s0 * fmaf(z.x, 1.f - s0, 1.f),
-                             o.y * y.y * s1 * fmaf(z.y, 1.f - s1, 1.f));
+            const float4 yv = *reinterpret_cast<const float4 *>(&s_dy[x]);
+            const float y[4] = {yv.x, yv.y, yv.z, yv.w};
+            float z[4], o[4];
+            piece_to_f32<BF16, 4, VEC>(rz, z);
+            piece_to_f32<BF16, 4, VEC>(rdo, o);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float sg = sigmoid_fast(z[k]);
+                o[k] *= y[k] * sg * fmaf(z[k], 1.f - sg, 1.f);
+            }
+            store_piece<BF16, 4, VEC>(p.dz, off, on, o);
         }
     }
 #pragma unroll
@@ -494,24 +514,33 @@ __global__ void __launch_bounds__(kScanThreads) scan_bwd_grad_kernel(const ScanB
     }
 }
 
-// dB, dC: the sum over the channel blocks of a group
-template <bool BF16>
+// dB, dC: the sum over the channel blocks of a group; W = 4 values a thread where a token's 2 n are whole fours
+template <bool BF16, int W>
 __global__ void __launch_bounds__(256) scan_bwd_bc_kernel(const ScanBwdParams p) {
     const int64_t per_token = (int64_t)p.G * 2 * p.n;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * W;
     if (i >= p.total_tokens * per_token) return;
     const int64_t t = i / per_token;
     const int x = static_cast<int>(i % per_token), g = x / (2 * p.n), w = x % (2 * p.n);
     const float *src = p.pBC + ((int64_t)g * p.cbg * p.total_tokens + t) * (2 * p.n) + w;
     const int64_t stride = p.total_tokens * 2 * p.n;
-    float s = 0.f;
-#pragma unroll 8
-    for (int b = 0; b < p.cbg; ++b) s += __ldg(src + b * stride);
-    store_out(w < p.n ? p.dB : p.dC, (t * p.G + g) * p.n + w % p.n, !BF16, s);
+    float s[W] = {};
+#pragma unroll 16
+    for (int b = 0; b < p.cbg; ++b) {
+        if constexpr (W == 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(src + b * stride));
+            s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+        } else {
+            s[0] += __ldg(src + b * stride);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+        store_out(w + k < p.n ? p.dB : p.dC, (t * p.G + g) * p.n + (w + k) % p.n, !BF16, s[k]);
 }
 
-// dA_log, dskip and ddt_bias: column sums over the records.  32 columns a block, 8 rows at a time.
-constexpr int kColRows = 8;
+// dA_log, dskip and ddt_bias: column sums over the records.  32 columns a block, kColRows rows at a time.
+constexpr int kColRows = 16;
 __global__ void __launch_bounds__(32 * kColRows) scan_bwd_weights_kernel(const ScanBwdParams p) {
     __shared__ float s_sum[kColRows][33];
     const int64_t nA = (int64_t)p.D * p.n;
@@ -523,7 +552,7 @@ __global__ void __launch_bounds__(32 * kColRows) scan_bwd_weights_kernel(const S
         if (col < nA) { src = p.H + col; stride = nA; }
         else if (col < nA + p.D) src = p.pskip + (col - nA);
         else src = p.pbias + (col - nA - p.D);
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t r = threadIdx.y; r < p.records; r += kColRows) s += src[r * stride];
     }
     s_sum[threadIdx.y][threadIdx.x] = s;
