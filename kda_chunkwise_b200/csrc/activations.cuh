@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "mma_frag.cuh"   // pack_bf16, cp_async
 
 namespace kda {
 
@@ -73,10 +74,6 @@ __device__ __forceinline__ void piece_to_f32(const Piece<BF16, N> &r, float (&v)
     }
 }
 
-__device__ __forceinline__ uint32_t pack2_bf16(float x, float y) {
-    return (uint32_t)f32_to_bf16(x) | ((uint32_t)f32_to_bf16(y) << 16);
-}
-
 // Rounds once to the storage type and stores the first `valid` of N elements (as load_piece).
 template <bool BF16, int N, bool VEC>
 __device__ __forceinline__ void store_piece(void *p, int64_t off, int valid, const float (&v)[N], int step = 1) {
@@ -91,7 +88,7 @@ __device__ __forceinline__ void store_piece(void *p, int64_t off, int valid, con
 #pragma unroll
             for (int k = 0; k < kOne / 4; ++k) {
                 const int e = i * (kOne / 4) + k;
-                if constexpr (BF16) x.w[k] = pack2_bf16(v[2 * e], v[2 * e + 1]);
+                if constexpr (BF16) x.w[k] = pack_bf16(v[2 * e], v[2 * e + 1]);
                 else x.w[k] = __float_as_uint(v[e]);
             }
             reinterpret_cast<V *>(dst)[i] = x.v;

@@ -6,9 +6,10 @@
 // The carried state is the last W - 1 inputs, [num_seqs, W - 1, C] in the inputs' type, oldest first.
 //
 // All three are bound by memory (about 10 flops a byte at most): each input is read once, its
-// neighbours in time come from registers, and a thread keeps several rows in flight.  A thread owns E
-// channels: consecutive ones, moved as one vector, where the rows allow it, else channels a block
-// apart, so that single elements are still read side by side.
+// neighbours in time come from registers, and a thread keeps several rows in flight, in a ring in shared
+// memory that it alone reads.  A thread owns E channels: consecutive ones, moved as one vector, where the
+// rows allow it, else channels a block apart, so that single elements are still read side by side (and
+// then a batch of rows in registers).
 #pragma once
 
 #include "activations.cuh"
@@ -46,6 +47,26 @@ struct ChannelGroup {
     template <bool RO = true>
     __device__ __forceinline__ void load(const void *p, int64_t row, bool on, Piece<BF16, E> &r) const {
         load_piece<BF16, E, VEC, RO>(p, row + c0, on ? count : 0, r, step);
+    }
+    // one row's vector into this thread's place of a ring slot, and back (VEC only)
+    static constexpr int kVec = E * (BF16 ? 2 : 4);   // bytes: 8 or 16
+    __device__ __forceinline__ void copy(unsigned char *slot, const void *p, int64_t row, bool on) const {
+        const bool in = on && count > 0;
+        const char *src = static_cast<const char *>(p) + (in ? (row + c0) * (BF16 ? 2 : 4) : 0);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(smem_u32(slot) + threadIdx.x * kVec), "l"(src),
+                     "n"(kVec), "r"(in ? kVec : 0) : "memory");
+    }
+    __device__ __forceinline__ void read(const unsigned char *slot, float (&v)[E]) const {
+        Piece<BF16, E> r;
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(slot + threadIdx.x * kVec);
+        if constexpr (kVec == 16) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(w);
+            r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(w);
+            r.w[0] = x.x; r.w[1] = x.y;
+        }
+        get(r, v);
     }
     __device__ __forceinline__ void get(const Piece<BF16, E> &r, float (&v)[E]) const { piece_to_f32<BF16, E, VEC>(r, v); }
     template <bool RO = true>
@@ -138,13 +159,15 @@ __device__ __forceinline__ void load_window(const ConvStateParams &p, const Grou
     }
 }
 
-constexpr int kConvRows = 8;   // rows in flight per thread, forward
+constexpr int kConvRows = 8;   // rows in flight per thread
 
 // grid: x = runs of run_len tokens, then one block per sequence for the final states; y = blocks of
 // channels.  With hN = h0 the two are separate launches (first_block skips the runs).
 template <bool BF16, int W, int E, bool VEC>
 __global__ void __launch_bounds__(kConvThreads) conv_state_fwd_kernel(const ConvStateParams p) {
     const ChannelGroup<BF16, E, VEC> cg(blockIdx.y, p.C);
+    constexpr int SLOT = kConvThreads * ChannelGroup<BF16, E, VEC>::kVec;
+    __shared__ __align__(16) unsigned char ring[VEC ? kConvRows * SLOT : 16];
     const int64_t bx = p.first_block + blockIdx.x;
     if (bx == 0 && blockIdx.y == 0) check_seqlens(p.cu, p.num_seqs, p.total_tokens);
     float xw[W > 1 ? W - 1 : 1][E];
@@ -157,32 +180,49 @@ __global__ void __launch_bounds__(kConvThreads) conv_state_fwd_kernel(const Conv
         for (int j = 0; j < W - 1; ++j) cg.store(p.hN, (seq * (W - 1) + j) * p.C, xw[j]);
         return;
     }
+    const int64_t r0 = bx * p.run_len, r1 = min64(r0 + p.run_len, p.total_tokens);
+    if constexpr (VEC) {
+#pragma unroll
+        for (int k = 0; k < kConvRows; ++k) {
+            cg.copy(ring + k * SLOT, p.x, (r0 + k) * p.C, r0 + k < r1);
+            cp_async_commit();
+        }
+    }
     float w[W][E], bias[E];
     load_taps<W, E>(p, cg, w, bias);
-    const int64_t r0 = bx * p.run_len, r1 = min64(r0 + p.run_len, p.total_tokens);
     int64_t seq = seq_of(p.cu, p.num_seqs, r0), s0, s1;
     seq_span(p.cu, (int)seq, p.num_seqs, p.total_tokens, s0, s1);
     load_window<W, E>(p, cg, r0, s0, seq, xw);
     for (int64_t t0 = r0; t0 < r1; t0 += kConvRows) {
-        Piece<BF16, E> rx[kConvRows];
+        Piece<BF16, E> rx[VEC ? 1 : kConvRows];
+        if constexpr (!VEC) {
 #pragma unroll
-        for (int k = 0; k < kConvRows; ++k) cg.load(p.x, (t0 + k) * p.C, t0 + k < r1, rx[k]);
+            for (int k = 0; k < kConvRows; ++k) cg.load(p.x, (t0 + k) * p.C, t0 + k < r1, rx[k]);
+        }
 #pragma unroll
         for (int k = 0; k < kConvRows; ++k) {
             const int64_t t = t0 + k;
             if (t >= r1) break;
+            float x[E], y[E];
+            if constexpr (VEC) {
+                cp_async_wait_group<kConvRows - 1>();
+                cg.read(ring + k * SLOT, x);
+                cg.copy(ring + k * SLOT, p.x, (t + kConvRows) * p.C, t + kConvRows < r1);
+                cp_async_commit();
+            } else {
+                cg.get(rx[k], x);
+            }
             if (t >= s1 && seq + 1 < p.num_seqs) {   // the next sequence that has tokens starts here
                 do seq_span(p.cu, (int)++seq, p.num_seqs, p.total_tokens, s0, s1);
                 while (t >= s1 && seq + 1 < p.num_seqs);
                 load_window<W, E>(p, cg, t, t, seq, xw);
             }
-            float x[E], y[E];
-            cg.get(rx[k], x);
             conv_row<W, E>(p, w, bias, xw, x, y);
             cg.store(p.y, t * p.C, y);
             slide<W, E>(xw, x);
         }
     }
+    cp_async_wait_all();
 }
 
 // One token of num_seqs sequences; the state (hN) in place.
@@ -204,8 +244,6 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(const ConvState
     }
 }
 
-constexpr int kConvBackRows = 4;   // rows of x and dy in flight per thread, backward
-
 // Gradients over runs of run_len tokens, one pass forwards in time: the gradient q of p is known at token t
 // from the window of inputs, and the input W - 1 tokens back is then complete,
 //   dx_u = sum_{i < W} w[W-1-i] q_{u+i}    (tokens of the same sequence only).
@@ -215,6 +253,8 @@ template <bool BF16, int W, int E, bool VEC>
 __global__ void __launch_bounds__(kConvThreads) conv_state_bwd_kernel(const ConvStateParams p) {
     const ChannelGroup<BF16, E, VEC> cg(blockIdx.y, p.C);
     if (blockIdx.x == 0 && blockIdx.y == 0) check_seqlens(p.cu, p.num_seqs, p.total_tokens);
+    constexpr int ROWS = kConvRows, SLOT = kConvThreads * ChannelGroup<BF16, E, VEC>::kVec;
+    __shared__ __align__(16) unsigned char ring[VEC ? 2 * ROWS * SLOT : 16];   // rows of x, of dy
     float w[W][E], bias[E], dw[W][E], db[E];
     load_taps<W, E>(p, cg, w, bias);
 #pragma unroll
@@ -246,20 +286,39 @@ __global__ void __launch_bounds__(kConvThreads) conv_state_bwd_kernel(const Conv
 #pragma unroll
             for (int i = 0; i < E; ++i) qw[j][i] = 0.f;
         const int64_t end = p1 + W - 1, stop = min64(end, s1);   // past `stop` there are no tokens
-        for (int64_t t0 = p0; t0 < end; t0 += kConvBackRows) {
-            Piece<BF16, E> rx[kConvBackRows], rd[kConvBackRows];
-#pragma unroll
-            for (int k = 0; k < kConvBackRows; ++k) {
-                cg.load(p.x, (t0 + k) * p.C, t0 + k < stop, rx[k]);
-                cg.load(p.dy, (t0 + k) * p.C, t0 + k < stop, rd[k]);
+        auto copy = [&](int slot, int64_t t) {
+            if constexpr (VEC) {
+                cg.copy(ring + slot * SLOT, p.x, t * p.C, t < stop);
+                cg.copy(ring + (ROWS + slot) * SLOT, p.dy, t * p.C, t < stop);
+                cp_async_commit();
             }
+        };
 #pragma unroll
-            for (int k = 0; k < kConvBackRows; ++k) {
+        for (int k = 0; k < ROWS; ++k) copy(k, p0 + k);
+        constexpr int BATCH = VEC ? ROWS : 4;
+        for (int64_t t0 = p0; t0 < end; t0 += BATCH) {
+            Piece<BF16, E> rx[VEC ? 1 : BATCH], rd[VEC ? 1 : BATCH];
+            if constexpr (!VEC) {
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    cg.load(p.x, (t0 + k) * p.C, t0 + k < stop, rx[k]);
+                    cg.load(p.dy, (t0 + k) * p.C, t0 + k < stop, rd[k]);
+                }
+            }
+#pragma unroll VEC ? 2 : BATCH
+            for (int k = 0; k < BATCH; ++k) {
                 const int64_t t = t0 + k;
                 if (t >= end) break;
-                float x[E], q[E];
-                cg.get(rx[k], x);
-                cg.get(rd[k], q);   // dy, then the gradient of p
+                float x[E], q[E];   // q: dy, then the gradient of p
+                if constexpr (VEC) {
+                    cp_async_wait_group<ROWS - 1>();
+                    cg.read(ring + k * SLOT, x);
+                    cg.read(ring + (ROWS + k) * SLOT, q);
+                    copy(k, t + ROWS);
+                } else {
+                    cg.get(rx[k], x);
+                    cg.get(rd[k], q);
+                }
                 if (t < stop) {
                     float a[E], sg[E];
 #pragma unroll
@@ -323,6 +382,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_state_bwd_kernel(const Conv
                 slide<W, E>(qw, q);
             }
         }
+        if constexpr (VEC) cp_async_wait_all();   // (the next sequence's rows go into the same slots)
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) {
