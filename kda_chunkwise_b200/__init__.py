@@ -167,7 +167,7 @@ def _check(status: int, where: str) -> None:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream_handle(stream, device) -> ctypes.c_void_p:
@@ -181,7 +181,7 @@ def _need(t, name, dtype, shape, device):
         raise ValueError(f"{name} is required")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
@@ -660,29 +660,39 @@ def chunk_kda(q, k, v, a, beta, A_log, cu_seqlens, gate=None, initial_state=None
 class _Call:
     """Where a call's work runs: its device is made current, and what it allocates belongs to its stream."""
 
+    __slots__ = ("device", "handle", "_with")
+
     def __init__(self, x, stream):
         if not x.is_cuda:
             raise ValueError(f"tensors must be on a CUDA device, got {x.device}")
-        self.device, self.stream, self._with = x.device, stream, []
-        if x.device.index != torch.cuda.current_device():
-            self._with.append(torch.cuda.device(x.device))
-        if stream is not None:
-            if stream.device != x.device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
-            self._with.append(torch.cuda.stream(stream))
+        self.device, self._with = x.device, None
+        index = x.get_device()
+        if stream is None:
+            self.handle = torch._C._cuda_getCurrentRawStream(index)
+        elif stream.device != x.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+        else:
+            self.handle = stream.cuda_stream
+        if stream is not None or index != torch.cuda.current_device():
+            # (a stream's context makes its device current too)
+            self._with = torch.cuda.device(x.device) if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        for w in self._with:
-            w.__enter__()
-        self.handle = _stream_handle(self.stream, self.device)
+        if self._with is not None:
+            self._with.__enter__()
         return self
 
     def __exit__(self, *exc):
-        for w in reversed(self._with):
-            w.__exit__(*exc)
+        if self._with is not None:
+            self._with.__exit__(*exc)
 
     def empty(self, shape, dtype):
         return torch.empty(shape, dtype=dtype, device=self.device)
+
+    @staticmethod
+    def like(t):
+        """An output of a checked (dense) tensor's shape and type; None for None."""
+        return None if t is None else torch.empty_like(t)
 
     def workspace(self, given, nbytes):
         if given is None:
@@ -751,7 +761,7 @@ def kda_selective_scan_fwd(u, dt, A_log, B, C, cu_seqlens, skip=None, z=None, dt
         _need(initial_state, "initial_state", f32, (N, D, n), u.device)
     with _Call(u, stream) as call:
         if out is None:
-            out = call.empty((T, D), u.dtype)
+            out = call.like(u)
         _need(out, "out", u.dtype, (T, D), u.device)
         if final_state is None and output_final_state:
             final_state = call.empty((N, D, n), f32)
@@ -772,7 +782,7 @@ def kda_selective_scan_step(u, dt, A_log, B, C, state, skip=None, z=None, dt_bia
     _need(state, "state", torch.float32, (N, D, n), u.device)
     with _Call(u, stream) as call:
         if out is None:
-            out = call.empty((N, D), u.dtype)
+            out = call.like(u)
         _need(out, "out", u.dtype, (N, D), u.device)
         st = lib.kda_selective_scan_step(_ptr(u), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(skip), _ptr(z),
                                          _ptr(dt_bias), _ptr(state), _ptr(out), code, N, D, n, G, call.handle)
@@ -794,11 +804,9 @@ def kda_selective_scan_bwd(u, dt, A_log, B, C, cu_seqlens, dout, skip=None, z=No
     if dfinal_state is not None:
         _need(dfinal_state, "dfinal_state", f32, (N, D, n), dev)
     with _Call(u, stream) as call:
-        given = lambda x, shape, dtype: None if x is None else call.empty(shape, dtype)  # noqa: E731
-        g = dict(du=call.empty((T, D), t), ddt=call.empty((T, D), t), dA_log=call.empty((D, n), f32),
-                 dB=call.empty((T, G, n), t), dC=call.empty((T, G, n), t), dskip=given(skip, (D,), f32),
-                 dz=given(z, (T, D), t), ddt_bias=given(dt_bias, (D,), f32),
-                 dinitial_state=given(initial_state, (N, D, n), f32))
+        g = dict(du=call.like(u), ddt=call.like(dt), dA_log=call.like(A_log), dB=call.like(B), dC=call.like(C),
+                 dskip=call.like(skip), dz=call.like(z), ddt_bias=call.like(dt_bias),
+                 dinitial_state=call.like(initial_state))
         ws, ws_bytes = call.workspace(workspace, kda_selective_scan_bwd_workspace_size(T, N, D, n, G))
         st = lib.kda_selective_scan_bwd(_ptr(u), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(skip), _ptr(z),
                                         _ptr(dt_bias), _ptr(cu_seqlens), N, T, D, n, G, _ptr(initial_state),
@@ -838,7 +846,7 @@ def kda_short_conv_fwd(x, w, cu_seqlens, bias=None, initial_state=None, silu: bo
         _need(initial_state, "initial_state", x.dtype, state, x.device)
     with _Call(x, stream) as call:
         if out is None:
-            out = call.empty((T, H, d), x.dtype)
+            out = call.like(x)
         _need(out, "out", x.dtype, (T, H, d), x.device)
         if final_state is None and output_final_state:
             final_state = call.empty(state, x.dtype)
@@ -857,7 +865,7 @@ def kda_short_conv_step(x, w, state, bias=None, silu: bool = False, l2norm: bool
     _need(state, "state", x.dtype, (N, W - 1, H, d), x.device)
     with _Call(x, stream) as call:
         if out is None:
-            out = call.empty((N, H, d), x.dtype)
+            out = call.like(x)
         _need(out, "out", x.dtype, (N, H, d), x.device)
         st = lib.kda_short_conv_step(_ptr(x), _ptr(w), _ptr(bias), _ptr(state), N, H, d, W, int(silu), int(l2norm),
                                      _ptr(out), code, call.handle)
@@ -876,15 +884,13 @@ def kda_short_conv_bwd(x, w, cu_seqlens, dy, bias=None, initial_state=None, dfin
     for what was not given."""
     T, H, d, W, code = _conv_args(x, w, bias)
     N = _need_seqlens(cu_seqlens, x.device)
-    state, t, f32 = (N, W - 1, H, d), x.dtype, torch.float32
+    state, t = (N, W - 1, H, d), x.dtype
     _need(dy, "dy", t, (T, H, d), x.device)
     for name, s in (("initial_state", initial_state), ("dfinal_state", dfinal_state)):
         if s is not None:
             _need(s, name, t, state, x.device)
     with _Call(x, stream) as call:
-        g = dict(dx=call.empty((T, H, d), t), dw=call.empty((H, d, W), f32),
-                 dbias=None if bias is None else call.empty((H, d), f32),
-                 dinitial_state=None if initial_state is None else call.empty(state, t))
+        g = dict(dx=call.like(x), dw=call.like(w), dbias=call.like(bias), dinitial_state=call.like(initial_state))
         ws, ws_bytes = call.workspace(workspace, kda_short_conv_bwd_workspace_size(T, H, d, W))
         st = lib.kda_short_conv_bwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(cu_seqlens), N, T, H, d, W, int(silu), int(l2norm),
                                     _ptr(initial_state), _ptr(dy), _ptr(dfinal_state), _ptr(g["dx"]), _ptr(g["dw"]),
@@ -911,9 +917,10 @@ def kda_layer_norm_fwd(x, w, b=None, eps: float = 1e-5, out=None, stream=None):
         _need(b, "b", torch.float32, (d,), x.device)
     with _Call(x, stream) as call:
         if out is None:
-            out = call.empty(x.shape, x.dtype)
+            out = call.like(x)
         _need(out, "out", x.dtype, x.shape, x.device)
-        mean, rstd = call.empty(lead, torch.float32), call.empty(lead, torch.float32)
+        mean = call.empty(lead, torch.float32)
+        rstd = call.like(mean)
         st = lib.kda_layer_norm_fwd(_ptr(x), _ptr(w), _ptr(b), rows, d, float(eps), _ptr(out), _ptr(mean), _ptr(rstd),
                                     code, call.handle)
     _check(st, "kda_layer_norm_fwd")
@@ -934,8 +941,7 @@ def kda_layer_norm_bwd(x, w, mean, rstd, dy, has_bias: bool = True, workspace=No
     _need(mean, "mean", torch.float32, lead, x.device)
     _need(rstd, "rstd", torch.float32, lead, x.device)
     with _Call(x, stream) as call:
-        g = dict(dx=call.empty(x.shape, x.dtype), dw=call.empty((d,), torch.float32),
-                 dbias=call.empty((d,), torch.float32) if has_bias else None)
+        g = dict(dx=call.like(x), dw=call.like(w), dbias=call.like(w) if has_bias else None)
         ws, ws_bytes = call.workspace(workspace, kda_layer_norm_bwd_workspace_size(rows, d))
         st = lib.kda_layer_norm_bwd(_ptr(x), _ptr(w), _ptr(mean), _ptr(rstd), _ptr(dy), rows, d, _ptr(g["dx"]),
                                     _ptr(g["dw"]), _ptr(g["dbias"]), code, _ptr(ws), ws_bytes, call.handle)

@@ -12,7 +12,10 @@
 // then a batch of rows in registers).
 #pragma once
 
+#include <type_traits>
+
 #include "activations.cuh"
+#include "f32x2.cuh"
 #include "preprocess.cuh"
 
 namespace kda {
@@ -56,7 +59,7 @@ struct ChannelGroup {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(smem_u32(slot) + threadIdx.x * kVec), "l"(src),
                      "n"(kVec), "r"(in ? kVec : 0) : "memory");
     }
-    __device__ __forceinline__ void read(const unsigned char *slot, float (&v)[E]) const {
+    __device__ __forceinline__ void read(const unsigned char *slot, f32x2 (&v)[E / 2]) const {
         Piece<BF16, E> r;
         const uint32_t *w = reinterpret_cast<const uint32_t *>(slot + threadIdx.x * kVec);
         if constexpr (kVec == 16) {
@@ -68,86 +71,129 @@ struct ChannelGroup {
         }
         get(r, v);
     }
-    __device__ __forceinline__ void get(const Piece<BF16, E> &r, float (&v)[E]) const { piece_to_f32<BF16, E, VEC>(r, v); }
+    // the channels in pairs, for the paired fp32 instructions
+    __device__ __forceinline__ void get(const Piece<BF16, E> &r, f32x2 (&v)[E / 2]) const {
+        float f[E];
+        piece_to_f32<BF16, E, VEC>(r, f);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) v[i] = f2_pack(f[2 * i], f[2 * i + 1]);
+    }
     template <bool RO = true>
-    __device__ __forceinline__ void load_f32(const void *p, int64_t row, bool on, float (&v)[E]) const {
+    __device__ __forceinline__ void load_f32(const void *p, int64_t row, bool on, f32x2 (&v)[E / 2]) const {
         Piece<BF16, E> r;
         load<RO>(p, row, on, r);
         get(r, v);
     }
-    __device__ __forceinline__ void store(void *p, int64_t row, const float (&v)[E]) const {
-        store_piece<BF16, E, VEC>(p, row + c0, count, v, step);
+    __device__ __forceinline__ void store(void *p, int64_t row, const f32x2 (&v)[E / 2]) const {
+        float f[E];
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) f2_unpack(v[i], f[2 * i], f[2 * i + 1]);
+        store_piece<BF16, E, VEC>(p, row + c0, count, f, step);
     }
 };
 
 // The taps of a thread's channels: W floats of a channel lie together, so that four taps are one load.
 template <int W, int E, class Group>
-__device__ __forceinline__ void load_taps(const ConvStateParams &p, const Group &cg, float (&w)[W][E], float (&bias)[E]) {
+__device__ __forceinline__ void load_taps(const ConvStateParams &p, const Group &cg, f32x2 (&w)[W][E / 2], f32x2 (&bias)[E / 2]) {
     const bool whole = (reinterpret_cast<uintptr_t>(p.w) & (W * 4 - 1)) == 0;   // (a power of two where it matters)
+    float wf[W][E], bf[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         const int64_t c = cg.c0 + i * cg.step;
         const bool on = i < cg.count;
-        bias[i] = on && p.bias ? __ldg(p.bias + c) : 0.f;
+        bf[i] = on && p.bias ? __ldg(p.bias + c) : 0.f;
         uint32_t r[W];
 #pragma unroll
         for (int j = 0; j < W; ++j) r[j] = 0u;
-        if constexpr (W == 2 || W == 4) {
-            if (whole) {
-                load_if<W * 4, true>(p.w + c * W, on, r);
+        if ((W == 2 || W == 4) && whole) {
+            if constexpr (W == 2 || W == 4) load_if<W * 4, true>(p.w + c * W, on, r);
+        } else {
 #pragma unroll
-                for (int j = 0; j < W; ++j) w[j][i] = __uint_as_float(r[j]);
-                continue;
-            }
+            for (int j = 0; j < W; ++j) load_if<4, true>(p.w + c * W + j, on, &r[j]);
         }
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = on ? __ldg(p.w + c * W + j) : 0.f;
+        for (int j = 0; j < W; ++j) wf[j][i] = __uint_as_float(r[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+        bias[i] = f2_pack(bf[2 * i], bf[2 * i + 1]);
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][i] = f2_pack(wf[j][2 * i], wf[j][2 * i + 1]);
     }
 }
 
-// sum over the lanes of one head (d / E lanes of a warp)
-__device__ __forceinline__ float head_sum(float v, int lanes) {
-    for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// sums over the lanes of one head (a power of two up to a warp)
+template <int N>
+__device__ __forceinline__ void head_sums(float (&v)[N], int lanes) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < lanes)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
-// One row's output from its window (xw[0] oldest) and input.
-template <int W, int E>
-__device__ __forceinline__ void conv_row(const ConvStateParams &p, const float (&w)[W][E], const float (&bias)[E],
-                                         const float (&xw)[W > 1 ? W - 1 : 1][E], const float (&x)[E], float (&y)[E]) {
+// the sigmoids of a pair
+__device__ __forceinline__ f32x2 sigmoids(f32x2 a) {
+    float x, y;
+    f2_unpack(a, x, y);
+    return f2_pack(sigmoid_fast(x), sigmoid_fast(y));
+}
+
+template <int N>
+__device__ __forceinline__ float pair_dot(const f32x2 (&a)[N], const f32x2 (&b)[N]) {
+    f32x2 s = f2_mul(a[0], b[0]);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        float a = bias[i];
+    for (int i = 1; i < N; ++i) s = f2_fma(a[i], b[i], s);
+    float x, y;
+    f2_unpack(s, x, y);
+    return x + y;
+}
+
+// One row's p from its window (xw[0] oldest) and input.
+template <int W, int N>
+__device__ __forceinline__ void conv_taps(const f32x2 (&w)[W][N], const f32x2 (&bias)[N], const f32x2 (&xw)[W > 1 ? W - 1 : 1][N],
+                                          const f32x2 (&x)[N], f32x2 (&a)[N]) {
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) a = fmaf(w[j][i], xw[j][i], a);
-        a = fmaf(w[W - 1][i], x[i], a);
-        y[i] = p.silu ? a * sigmoid_fast(a) : a;
+    for (int i = 0; i < N; ++i) {
+        a[i] = bias[i];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) a[i] = f2_fma(w[j][i], xw[j][i], a[i]);
+        a[i] = f2_fma(w[W - 1][i], x[i], a[i]);
     }
+}
+
+// One row's output.
+template <int W, int N>
+__device__ __forceinline__ void conv_row(const ConvStateParams &p, const f32x2 (&w)[W][N], const f32x2 (&bias)[N],
+                                         const f32x2 (&xw)[W > 1 ? W - 1 : 1][N], const f32x2 (&x)[N], f32x2 (&y)[N], int lanes) {
+    conv_taps<W, N>(w, bias, xw, x, y);
+    if (p.silu)
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = f2_mul(y[i], sigmoids(y[i]));
     if (p.l2norm) {
-        float ss = 0.f;
+        float ss[1] = {pair_dot(y, y)};
+        head_sums(ss, lanes);
+        const f32x2 inv = f2_splat(rsqrtf(ss[0] + 1e-12f));
 #pragma unroll
-        for (int i = 0; i < E; ++i) ss = fmaf(y[i], y[i], ss);
-        const float inv = rsqrtf(head_sum(ss, p.d / E) + 1e-12f);
-#pragma unroll
-        for (int i = 0; i < E; ++i) y[i] *= inv;
+        for (int i = 0; i < N; ++i) y[i] = f2_mul(y[i], inv);
     }
 }
 
-template <int W, int E>
-__device__ __forceinline__ void slide(float (&xw)[W > 1 ? W - 1 : 1][E], const float (&x)[E]) {
+template <int W, int N>
+__device__ __forceinline__ void slide(f32x2 (&xw)[W > 1 ? W - 1 : 1][N], const f32x2 (&x)[N]) {
 #pragma unroll
     for (int j = 0; j + 1 < W - 1; ++j)
 #pragma unroll
-        for (int i = 0; i < E; ++i) xw[j][i] = xw[j + 1][i];
+        for (int i = 0; i < N; ++i) xw[j][i] = xw[j + 1][i];
     if (W > 1)
 #pragma unroll
-        for (int i = 0; i < E; ++i) xw[W > 1 ? W - 2 : 0][i] = x[i];
+        for (int i = 0; i < N; ++i) xw[W > 1 ? W - 2 : 0][i] = x[i];
 }
 
 // The window before token t of a sequence starting at s0: inputs, or rows of its carried state.
 template <int W, int E, class Group>
 __device__ __forceinline__ void load_window(const ConvStateParams &p, const Group &cg, int64_t t, int64_t s0,
-                                            int64_t seq, float (&xw)[W > 1 ? W - 1 : 1][E]) {
+                                            int64_t seq, f32x2 (&xw)[W > 1 ? W - 1 : 1][E / 2]) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
         const int64_t tt = t - (W - 1) + j;
@@ -159,18 +205,45 @@ __device__ __forceinline__ void load_window(const ConvStateParams &p, const Grou
     }
 }
 
-constexpr int kConvRows = 8;   // rows in flight per thread
+constexpr int kConvRows = 8;     // rows in flight per thread
+constexpr int kConvUnroll = 6;   // rows of one turn of a loop: a multiple of every window, so that sliding is renaming
+
+// Rows on their way: a ring whose slot i % kConvRows holds row i of a run, or (not VEC) the rows of one turn in
+// registers.
+template <bool BF16, int E, bool VEC>
+struct ConvRows {
+    using Group = ChannelGroup<BF16, E, VEC>;
+    static constexpr int kSlot = kConvThreads * Group::kVec;
+    static constexpr int kBytes = VEC ? kConvRows * kSlot : 16;
+    unsigned char *ring;
+    const void *p;
+    Piece<BF16, E> rows[VEC ? 1 : kConvUnroll];
+    __device__ __forceinline__ void copy(const Group &cg, int i, int64_t row, bool on) {
+        if constexpr (VEC) cg.copy(ring + i % kConvRows * kSlot, p, row, on);
+    }
+    __device__ __forceinline__ void fetch(const Group &cg, int k, int64_t row, bool on) {
+        if constexpr (!VEC) cg.load(p, row, on, rows[k]);
+    }
+    __device__ __forceinline__ void read(const Group &cg, int i, int k, f32x2 (&v)[E / 2]) const {
+        if constexpr (VEC) cg.read(ring + i % kConvRows * kSlot, v);
+        else cg.get(rows[k], v);
+    }
+};
 
 // grid: x = runs of run_len tokens, then one block per sequence for the final states; y = blocks of
 // channels.  With hN = h0 the two are separate launches (first_block skips the runs).
 template <bool BF16, int W, int E, bool VEC>
 __global__ void __launch_bounds__(kConvThreads) conv_state_fwd_kernel(const ConvStateParams p) {
+    constexpr int N = E / 2;
+    using Rows = ConvRows<BF16, E, VEC>;
+    __shared__ __align__(16) unsigned char slots[Rows::kBytes];
     const ChannelGroup<BF16, E, VEC> cg(blockIdx.y, p.C);
-    constexpr int SLOT = kConvThreads * ChannelGroup<BF16, E, VEC>::kVec;
-    __shared__ __align__(16) unsigned char ring[VEC ? kConvRows * SLOT : 16];
+    Rows xs;
+    xs.ring = slots;
+    xs.p = p.x;
     const int64_t bx = p.first_block + blockIdx.x;
     if (bx == 0 && blockIdx.y == 0) check_seqlens(p.cu, p.num_seqs, p.total_tokens);
-    float xw[W > 1 ? W - 1 : 1][E];
+    f32x2 xw[W > 1 ? W - 1 : 1][N];
     if (bx >= p.runs) {   // the state after a sequence: its last W - 1 inputs, all read before any is written
         const int64_t seq = bx - p.runs;
         int64_t s0, s1;
@@ -181,63 +254,68 @@ __global__ void __launch_bounds__(kConvThreads) conv_state_fwd_kernel(const Conv
         return;
     }
     const int64_t r0 = bx * p.run_len, r1 = min64(r0 + p.run_len, p.total_tokens);
-    if constexpr (VEC) {
+    const int rows = static_cast<int>(r1 - r0);
 #pragma unroll
-        for (int k = 0; k < kConvRows; ++k) {
-            cg.copy(ring + k * SLOT, p.x, (r0 + k) * p.C, r0 + k < r1);
-            cp_async_commit();
-        }
+    for (int k = 0; k < kConvRows; ++k) {
+        xs.copy(cg, k, (r0 + k) * p.C, k < rows);
+        cp_async_commit();
     }
-    float w[W][E], bias[E];
+    const int lanes = p.d / E;
+    f32x2 w[W][N], bias[N];
     load_taps<W, E>(p, cg, w, bias);
     int64_t seq = seq_of(p.cu, p.num_seqs, r0), s0, s1;
     seq_span(p.cu, (int)seq, p.num_seqs, p.total_tokens, s0, s1);
     load_window<W, E>(p, cg, r0, s0, seq, xw);
-    for (int64_t t0 = r0; t0 < r1; t0 += kConvRows) {
-        Piece<BF16, E> rx[VEC ? 1 : kConvRows];
-        if constexpr (!VEC) {
+    int64_t at = r0 * p.C;   // of row i
+    auto row = [&](int i, int k) {   // the k-th of a turn
+        f32x2 x[N], y[N];
+        cp_async_wait_group<kConvRows - 1>();
+        xs.read(cg, i, k, x);
+        xs.copy(cg, i, at + (int64_t)kConvRows * p.C, i + kConvRows < rows);
+        cp_async_commit();
+        conv_row<W, N>(p, w, bias, xw, x, y, lanes);
+        cg.store(p.y, at, y);
+        slide<W, N>(xw, x);
+        at += p.C;
+    };
+    int i = 0;
+    while (true) {
+        // rows of this sequence
+        const int end = seq + 1 < p.num_seqs ? static_cast<int>(min64(s1 > r0 ? s1 - r0 : 0, rows)) : rows;
+        for (; i + kConvUnroll <= end; i += kConvUnroll) {
 #pragma unroll
-            for (int k = 0; k < kConvRows; ++k) cg.load(p.x, (t0 + k) * p.C, t0 + k < r1, rx[k]);
-        }
+            for (int k = 0; k < kConvUnroll; ++k) xs.fetch(cg, k, at + (int64_t)k * p.C, true);
 #pragma unroll
-        for (int k = 0; k < kConvRows; ++k) {
-            const int64_t t = t0 + k;
-            if (t >= r1) break;
-            float x[E], y[E];
-            if constexpr (VEC) {
-                cp_async_wait_group<kConvRows - 1>();
-                cg.read(ring + k * SLOT, x);
-                cg.copy(ring + k * SLOT, p.x, (t + kConvRows) * p.C, t + kConvRows < r1);
-                cp_async_commit();
-            } else {
-                cg.get(rx[k], x);
-            }
-            if (t >= s1 && seq + 1 < p.num_seqs) {   // the next sequence that has tokens starts here
-                do seq_span(p.cu, (int)++seq, p.num_seqs, p.total_tokens, s0, s1);
-                while (t >= s1 && seq + 1 < p.num_seqs);
-                load_window<W, E>(p, cg, t, t, seq, xw);
-            }
-            conv_row<W, E>(p, w, bias, xw, x, y);
-            cg.store(p.y, t * p.C, y);
-            slide<W, E>(xw, x);
+            for (int k = 0; k < kConvUnroll; ++k) row(i + k, k);
         }
+#pragma unroll 1
+        for (; i < end; ++i) {
+            xs.fetch(cg, 0, at, true);
+            row(i, 0);
+        }
+        if (i >= rows) break;
+        do seq_span(p.cu, (int)++seq, p.num_seqs, p.total_tokens, s0, s1);   // the next sequence that has tokens starts here
+        while (r0 + i >= s1 && seq + 1 < p.num_seqs);
+        load_window<W, E>(p, cg, r0 + i, r0 + i, seq, xw);
     }
     cp_async_wait_all();
 }
 
-// One token of num_seqs sequences; the state (hN) in place.
+// One token of num_seqs sequences; the state (hN) in place.  A block walks over rows of the batch.
 template <bool BF16, int W, int E, bool VEC>
 __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(const ConvStateParams p) {
+    constexpr int N = E / 2;
     const ChannelGroup<BF16, E, VEC> cg(blockIdx.y, p.C);
-    float w[W][E], bias[E];
+    const int lanes = p.d / E;
+    f32x2 w[W][N], bias[N];
     load_taps<W, E>(p, cg, w, bias);
     for (int64_t r = blockIdx.x; r < p.num_seqs; r += gridDim.x) {
-        float xw[W > 1 ? W - 1 : 1][E], x[E], y[E];
+        f32x2 xw[W > 1 ? W - 1 : 1][N], x[N], y[N];
         cg.load_f32(p.x, r * p.C, true, x);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) cg.template load_f32<false>(p.h0, (r * (W - 1) + j) * p.C, true, xw[j]);
-        conv_row<W, E>(p, w, bias, xw, x, y);
-        slide<W, E>(xw, x);
+        conv_row<W, N>(p, w, bias, xw, x, y, lanes);
+        slide<W, N>(xw, x);
         cg.store(p.y, r * p.C, y);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) cg.store(p.hN, (r * (W - 1) + j) * p.C, xw[j]);
@@ -251,18 +329,26 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(const ConvState
 // first token are the rows of its carried state.
 template <bool BF16, int W, int E, bool VEC>
 __global__ void __launch_bounds__(kConvThreads) conv_state_bwd_kernel(const ConvStateParams p) {
+    constexpr int N = E / 2;
+    using Rows = ConvRows<BF16, E, VEC>;
+    __shared__ __align__(16) unsigned char slots[2 * Rows::kBytes];
     const ChannelGroup<BF16, E, VEC> cg(blockIdx.y, p.C);
+    Rows xs, ds;   // of x, of dy
+    xs.ring = slots;
+    ds.ring = slots + Rows::kBytes;
+    xs.p = p.x;
+    ds.p = p.dy;
     if (blockIdx.x == 0 && blockIdx.y == 0) check_seqlens(p.cu, p.num_seqs, p.total_tokens);
-    constexpr int ROWS = kConvRows, SLOT = kConvThreads * ChannelGroup<BF16, E, VEC>::kVec;
-    __shared__ __align__(16) unsigned char ring[VEC ? 2 * ROWS * SLOT : 16];   // rows of x, of dy
-    float w[W][E], bias[E], dw[W][E], db[E];
+    const int lanes = p.d / E;
+    f32x2 w[W][N], bias[N], dw[W][N], db[N];
     load_taps<W, E>(p, cg, w, bias);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        db[i] = 0.f;
+    for (int i = 0; i < N; ++i) {
+        db[i] = 0ull;
 #pragma unroll
-        for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
+        for (int j = 0; j < W; ++j) dw[j][i] = 0ull;
     }
+    const f32x2 one = f2_splat(1.f), minus = f2_splat(-1.f);
     const int64_t r0 = blockIdx.x * p.run_len, r1 = min64(r0 + p.run_len, p.total_tokens);
     const bool last_run = r1 == p.total_tokens;
     // the first sequence that ends past r0 or is empty and starts there
@@ -279,118 +365,114 @@ __global__ void __launch_bounds__(kConvThreads) conv_state_bwd_kernel(const Conv
         if (s0 == s1 && s0 < r0) continue;
         const int64_t p0 = s0 > r0 ? s0 : r0, p1 = min64(s1, r1);   // this run's tokens of the sequence
         if (p0 > p1 || (p0 == p1 && s0 != s1)) continue;
-        float xw[W > 1 ? W - 1 : 1][E], qw[W > 1 ? W - 1 : 1][E];   // inputs and gradients of the last W - 1 tokens
+        // rows i = 0 .. from p0 on: own of them are this run's, with_data have tokens, end complete the inputs
+        const int own = static_cast<int>(p1 - p0), end = own + W - 1, with_data = static_cast<int>(min64(end, s1 - p0));
+        f32x2 xw[W > 1 ? W - 1 : 1][N], qw[W > 1 ? W - 1 : 1][N];   // inputs and gradients of the last W - 1 tokens
         load_window<W, E>(p, cg, p0, s0, seq, xw);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-            for (int i = 0; i < E; ++i) qw[j][i] = 0.f;
-        const int64_t end = p1 + W - 1, stop = min64(end, s1);   // past `stop` there are no tokens
-        auto copy = [&](int slot, int64_t t) {
-            if constexpr (VEC) {
-                cg.copy(ring + slot * SLOT, p.x, t * p.C, t < stop);
-                cg.copy(ring + (ROWS + slot) * SLOT, p.dy, t * p.C, t < stop);
-                cp_async_commit();
-            }
+            for (int i = 0; i < N; ++i) qw[j][i] = 0ull;
+        int64_t at = p0 * p.C;   // of row i
+        auto copy = [&](int i, int64_t off) {
+            xs.copy(cg, i, off, i < with_data);
+            ds.copy(cg, i, off, i < with_data);
+            cp_async_commit();
+        };
+        auto fetch = [&](int i, int k, int64_t off) {
+            xs.fetch(cg, k, off, i < with_data);
+            ds.fetch(cg, k, off, i < with_data);
         };
 #pragma unroll
-        for (int k = 0; k < ROWS; ++k) copy(k, p0 + k);
-        constexpr int BATCH = VEC ? ROWS : 4;
-        for (int64_t t0 = p0; t0 < end; t0 += BATCH) {
-            Piece<BF16, E> rx[VEC ? 1 : BATCH], rd[VEC ? 1 : BATCH];
-            if constexpr (!VEC) {
+        for (int k = 0; k < kConvRows; ++k) copy(k, at + (int64_t)k * p.C);
+        // INNER: an own row whose complete input is an own one too, and no row of the final state
+        auto row = [&](int i, int turn, auto inner) {   // the turn-th row of a turn
+            constexpr bool INNER = decltype(inner)::value;
+            f32x2 x[N], q[N];   // q: dy, then the gradient of p
+            cp_async_wait_group<kConvRows - 1>();
+            xs.read(cg, i, turn, x);
+            ds.read(cg, i, turn, q);
+            copy(i + kConvRows, at + (int64_t)kConvRows * p.C);
+            if (INNER || i < with_data) {
+                f32x2 a[N], sg[N];
+                conv_taps<W, N>(w, bias, xw, x, a);
 #pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    cg.load(p.x, (t0 + k) * p.C, t0 + k < stop, rx[k]);
-                    cg.load(p.dy, (t0 + k) * p.C, t0 + k < stop, rd[k]);
+                for (int k = 0; k < N; ++k) sg[k] = p.silu ? sigmoids(a[k]) : one;
+                if (p.l2norm) {   // y = s inv:  ds = inv (dy - y (y . dy)) = inv dy - s inv^3 (s . dy)
+                    f32x2 s[N];
+#pragma unroll
+                    for (int k = 0; k < N; ++k) s[k] = f2_mul(a[k], sg[k]);
+                    float sum[2] = {pair_dot(s, s), pair_dot(s, q)};
+                    head_sums(sum, lanes);
+                    const float inv = rsqrtf(sum[0] + 1e-12f);
+                    const f32x2 iv = f2_splat(inv), k2 = f2_splat(-inv * inv * sum[1]);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) q[k] = f2_mul(iv, f2_fma(k2, s[k], q[k]));
                 }
+                if (p.silu)   // silu' = sg (1 + a (1 - sg))
+#pragma unroll
+                    for (int k = 0; k < N; ++k) q[k] = f2_mul(q[k], f2_mul(sg[k], f2_fma(a[k], f2_fma(sg[k], minus, one), one)));
+                if (INNER || i < own)
+#pragma unroll
+                    for (int k = 0; k < N; ++k) {
+                        db[k] = f2_add(db[k], q[k]);
+#pragma unroll
+                        for (int j = 0; j < W - 1; ++j) dw[j][k] = f2_fma(q[k], xw[j][k], dw[j][k]);
+                        dw[W - 1][k] = f2_fma(q[k], x[k], dw[W - 1][k]);
+                    }
             }
-#pragma unroll VEC ? 2 : BATCH
-            for (int k = 0; k < BATCH; ++k) {
-                const int64_t t = t0 + k;
-                if (t >= end) break;
-                float x[E], q[E];   // q: dy, then the gradient of p
-                if constexpr (VEC) {
-                    cp_async_wait_group<ROWS - 1>();
-                    cg.read(ring + k * SLOT, x);
-                    cg.read(ring + (ROWS + k) * SLOT, q);
-                    copy(k, t + ROWS);
-                } else {
-                    cg.get(rx[k], x);
-                    cg.get(rd[k], q);
+            const bool carried = i < W - 1;   // the input completed now is a row of the carried state, if any
+            if (INNER || !carried || (p0 == s0 && p.dh0)) {
+                f32x2 dx[N];
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    dx[k] = f2_mul(w[0][k], q[k]);
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) dx[k] = f2_fma(w[W - 1 - j][k], qw[j][k], dx[k]);
                 }
-                if (t < stop) {
-                    float a[E], sg[E];
+                if (!INNER && p.dhN && p0 + i >= s1) {   // it is also row p0 + i - s1 of the final state
+                    f32x2 e[N];
+                    cg.load_f32(p.dhN, (seq * (W - 1) + (p0 + i - s1)) * p.C, true, e);
 #pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        float v = bias[i];
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) v = fmaf(w[j][i], xw[j][i], v);
-                        a[i] = fmaf(w[W - 1][i], x[i], v);
-                        sg[i] = p.silu ? sigmoid_fast(a[i]) : 1.f;
-                    }
-                    if (p.l2norm) {   // y = s inv:  ds = inv (dy - y (y . dy))
-                        float ss = 0.f, sd = 0.f;
-#pragma unroll
-                        for (int i = 0; i < E; ++i) {
-                            const float s = p.silu ? a[i] * sg[i] : a[i];
-                            ss = fmaf(s, s, ss);
-                            sd = fmaf(s, q[i], sd);
-                        }
-                        const int lanes = p.d / E;
-                        for (int o = lanes / 2; o > 0; o >>= 1) {
-                            ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                            sd += __shfl_xor_sync(0xffffffffu, sd, o);
-                        }
-                        const float inv = rsqrtf(ss + 1e-12f), k2 = inv * inv * sd;
-#pragma unroll
-                        for (int i = 0; i < E; ++i) q[i] = inv * fmaf(-k2, p.silu ? a[i] * sg[i] : a[i], q[i]);
-                    }
-                    if (p.silu)
-#pragma unroll
-                        for (int i = 0; i < E; ++i) q[i] *= sg[i] * fmaf(a[i], 1.f - sg[i], 1.f);
-                    if (t < p1)
-#pragma unroll
-                        for (int i = 0; i < E; ++i) {
-                            db[i] += q[i];
-#pragma unroll
-                            for (int j = 0; j < W - 1; ++j) dw[j][i] = fmaf(q[i], xw[j][i], dw[j][i]);
-                            dw[W - 1][i] = fmaf(q[i], x[i], dw[W - 1][i]);
-                        }
+                    for (int k = 0; k < N; ++k) dx[k] = f2_add(dx[k], e[k]);
                 }
-                const int64_t pos = t - (W - 1);   // complete now
-                if (pos >= p0 || (p0 == s0 && p.dh0)) {
-                    float dx[E];
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        float v = w[0][i] * q[i];
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) v = fmaf(w[W - 1 - j][i], qw[j][i], v);
-                        dx[i] = v;
-                    }
-                    const int64_t f = pos - s1 + W - 1;   // row of the final state that holds this input
-                    if (f >= 0 && p.dhN) {
-                        float e[E];
-                        cg.load_f32(p.dhN, (seq * (W - 1) + f) * p.C, true, e);
-#pragma unroll
-                        for (int i = 0; i < E; ++i) dx[i] += e[i];
-                    }
-                    if (pos >= p0) cg.store(p.y, pos * p.C, dx);
-                    else cg.store(p.dh0, (seq * (W - 1) + (pos - s0 + W - 1)) * p.C, dx);
-                }
-                slide<W, E>(xw, x);
-                slide<W, E>(qw, q);
+                if (INNER || !carried) cg.store(p.y, at - (int64_t)(W - 1) * p.C, dx);
+                else cg.store(p.dh0, (seq * (W - 1) + i) * p.C, dx);
             }
+            slide<W, N>(xw, x);
+            slide<W, N>(qw, q);
+            at += p.C;
+        };
+        int i = 0;
+        auto edge = [&](int last) {
+#pragma unroll 1
+            for (; i < last; ++i) {
+                fetch(i, 0, at);
+                row(i, 0, std::false_type());
+            }
+        };
+        edge(W - 1 < end ? W - 1 : end);
+        for (; i + kConvUnroll <= own; i += kConvUnroll) {
+#pragma unroll
+            for (int k = 0; k < kConvUnroll; ++k) fetch(i + k, k, at + (int64_t)k * p.C);
+#pragma unroll
+            for (int k = 0; k < kConvUnroll; ++k) row(i + k, k, std::true_type());
         }
-        if constexpr (VEC) cp_async_wait_all();   // (the next sequence's rows go into the same slots)
+        edge(end);
+        cp_async_wait_all();   // (the next sequence's rows go into the same slots)
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         if (i >= cg.count) break;
         float *dst = p.part + (int64_t)blockIdx.x * (W + 1) * p.C + cg.c0 + i * cg.step;
+        float v[2];
 #pragma unroll
-        for (int j = 0; j < W; ++j) dst[(int64_t)j * p.C] = dw[j][i];
-        dst[(int64_t)W * p.C] = db[i];
+        for (int j = 0; j < W; ++j) {
+            f2_unpack(dw[j][i / 2], v[0], v[1]);
+            dst[(int64_t)j * p.C] = v[i & 1];
+        }
+        f2_unpack(db[i / 2], v[0], v[1]);
+        dst[(int64_t)W * p.C] = v[i & 1];
     }
 }
 
