@@ -1301,12 +1301,15 @@ bool scan_sizes_ok(int64_t rows, int32_t seqs, int32_t D, int32_t n, int32_t G) 
 }
 
 // Tokens of a segment of the prompt's scan; more than total_tokens where sequences are not cut (so that
-// an empty sequence at the very end has its record too).
+// an empty sequence at the very end has its record too).  A block takes an SM, so cutting pays where at least
+// two segments of every sequence run side by side (it takes their exponentials twice): as many as fill the SMs
+// once, of two tiles or more.  8192 tokens x 16 states, uncut against cut: 256 channels 290 and 47 us
+// (16 segments), 1024 channels 297 and 141 (4), 2048 channels 307 and 274 (2).
 int64_t scan_segment_len(int64_t T, int32_t num_seqs, int32_t D, int32_t n, int32_t G) {
-    const int64_t blocks = (int64_t)G * scan_blocks_of_group(D, n, G, 1), sms = device_sm_count();
-    if (2 * blocks * num_seqs >= sms) return T + 1;
-    const int64_t want = std::max<int64_t>(1, 2 * sms / blocks);   // segments of the whole batch
-    const int64_t len = std::max<int64_t>(256, ((T + want - 1) / want + 63) / 64 * 64);
+    const int64_t blocks = (int64_t)G * scan_blocks_of_group(D, n, G, 1);
+    const int64_t each = device_sm_count() / (blocks * num_seqs);
+    if (each < 2) return T + 1;
+    const int64_t len = std::max<int64_t>(128, ((T + each * num_seqs - 1) / (each * num_seqs) + 63) / 64 * 64);
     return len >= T ? T + 1 : len;
 }
 
@@ -1428,6 +1431,7 @@ kda_status kda_selective_scan_fwd(const void *u, const void *dt, const float *A_
     const int64_t blocks = space.records * G * p.cbg;
     if (blocks > 0x7fffffffLL) return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_fwd: too many sequences and channels");
     const bool cut = space.total > 0;
+    p.by_length = !cut && num_seqs > 1 && num_seqs <= kda::kRankSeqs && blocks > device_sm_count();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return with_dtype(dtype, [&](auto bf16) {
         return with_lanes(n, [&](auto lanes) {

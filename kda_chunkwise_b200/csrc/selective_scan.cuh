@@ -55,6 +55,7 @@ struct ScanParams {
     int64_t seg_len;
     bool vec;                           // channels of u, dt, z and out may be moved in fours
     bool vecn;                          // n is a multiple of four
+    bool by_length;                     // blocks of long sequences first
 };
 
 // The segment that record `rec` stands for: record base(s) + j, base(s) = cu[s] / seg_len + s, is the
@@ -79,6 +80,27 @@ __device__ __forceinline__ bool scan_segment(const int32_t *cu, int num_seqs, in
     t1 = min64(t0 + seg_len, s1);
     last = t1 == s1;
     return true;
+}
+
+// The sequence with `rank` longer ones before it, in uncut batches of up to kRankSeqs sequences: blocks of long
+// sequences start first, so that the last ones to end are short.  All threads of the block call it.
+constexpr int kRankSeqs = 64;
+__device__ __forceinline__ int sequence_of_rank(const int32_t *cu, int num_seqs, int rank) {
+    __shared__ int s_seq;
+    if (threadIdx.x == 0) s_seq = rank;
+    __syncthreads();
+    const int i = threadIdx.x;
+    if (i < num_seqs) {
+        const int64_t len = (int64_t)cu[i + 1] - cu[i];
+        int before = 0;
+        for (int k = 0; k < num_seqs; ++k) {
+            const int64_t other = (int64_t)cu[k + 1] - cu[k];
+            before += other > len || (other == len && k < i);
+        }
+        if (before == rank) s_seq = i;
+    }
+    __syncthreads();
+    return s_seq;
 }
 
 // four states (or weights) of one channel from column m0 on; those past n are zero
@@ -229,9 +251,9 @@ struct ScanSmem {
 // Asynchronous copy of four elements to shared memory, or zeros past `on` of them.  bf16 that may not be
 // moved as a vector is read and stored at once.
 template <bool BF16>
-__device__ __forceinline__ void copy_four(void *dst, const void *p, int64_t off, int on, bool vec) {
+__device__ __forceinline__ void copy_four(void *dst, const void *tensor, const char *at, int on, bool vec) {
     constexpr int kElem = BF16 ? 2 : 4, kBytes = 4 * kElem;
-    const char *src = static_cast<const char *>(p) + (on > 0 ? off * kElem : 0);
+    const char *src = on > 0 ? at : static_cast<const char *>(tensor);   // (an address that may be named)
     const uint32_t to = smem_u32(dst);
     if (vec) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(to), "l"(src), "n"(kBytes), "r"(on > 0 ? kBytes : 0) : "memory");
@@ -277,8 +299,9 @@ __global__ void __launch_bounds__(kScanThreads + kStageThreads, 1) scan_fwd_kern
 
     if (blockIdx.x == 0 && !SUMMARY) check_seqlens(p.cu, p.num_seqs, p.total_tokens);
     const int ncb = p.G * p.cbg;
-    const int64_t rec = blockIdx.x / ncb;
+    int64_t rec = blockIdx.x / ncb;
     const int cb = blockIdx.x % ncb;
+    if (p.by_length) rec = sequence_of_rank(p.cu, p.num_seqs, static_cast<int>(rec));   // (uncut: a record is a sequence)
     const int DG = p.D / p.G, g = cb / p.cbg, cbase = (cb % p.cbg) * CH;   // first channel of the block within its group
     int seq;
     int64_t j, t0, t1;
@@ -291,61 +314,70 @@ __global__ void __launch_bounds__(kScanThreads + kStageThreads, 1) scan_fwd_kern
     if (threadIdx.x >= kScanThreads) {
         // ---- staging ----
         const int tid = threadIdx.x - kScanThreads;
-        // four i of this thread: its row, and the channels within the block (the same for every i)
-        auto row_of = [&](int i) { return tid / FR + i * (kStageThreads / FR); };   // (past the tile where there are more threads than fours)
-        const int col = 4 * (tid % FR), left = DG - cbase - col, four_on = left > 0 ? (left > 4 ? 4 : left) : 0;
-        auto on_of = [&](int i, int64_t t) { return t < t1 && row_of(i) < TT ? four_on : 0; };   // how many of them exist at token t
+        // four i of this thread: row row0 + i kRowStep of a tile (past it where there are more threads than
+        // fours), and the channels within the block, the same for every i
+        constexpr int kElem = BF16 ? 2 : 4, kRowStep = kStageThreads / FR;
+        const int row0 = tid / FR, col = 4 * (tid % FR), left = DG - cbase - col, four_on = left > 0 ? (left > 4 ? 4 : left) : 0;
+        const int len = static_cast<int>(t1 - t0);
+        // how many channels of four i exist in the tile whose first token is t0 + t
+        auto on_of = [&](int i, int t) { return row0 + i * kRowStep < TT && t + row0 + i * kRowStep < len ? four_on : 0; };
         float bias[4], skip[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             bias[k] = p.dt_bias && four_on > k ? p.dt_bias[c0 + col + k] : 0.f;
             skip[k] = p.skip && four_on > k ? p.skip[c0 + col + k] : 0.f;
         }
-        // this thread's part of a ring slot: fours of u, dt and z, and of B and C
-        unsigned char *ring = scan_tiles + 2 * SM::kBuf;
-        auto raw = [&](int tile, int which) {
-            return ring + (tile % NS) * SM::kRaw + (which * kStageThreads + tid) * SM::kFour;
+        // This thread's part of a ring slot: fours of u, dt and z, and of B and C.  Offsets (in bytes of global memory,
+        // in slots of the ring) move along with the tiles.
+        unsigned char *const ring = scan_tiles + 2 * SM::kBuf + tid * SM::kFour;
+        auto raw = [&](int slot, int which) { return ring + slot * SM::kRaw + which * (kStageThreads * SM::kFour); };
+        unsigned char *const ring_bc = scan_tiles + 2 * SM::kBuf + 3 * R * kStageThreads * SM::kFour + tid * sizeof(QuadBC<BF16>);
+        auto raw_bc = [&](int slot, int q) {
+            return reinterpret_cast<QuadBC<BF16> *>(ring_bc + slot * SM::kRaw + q * (kStageThreads * sizeof(QuadBC<BF16>)));
         };
-        auto raw_bc = [&](int tile, int q) {
-            return reinterpret_cast<QuadBC<BF16> *>(ring + (tile % NS) * SM::kRaw + 3 * R * kStageThreads * SM::kFour) + q * kStageThreads + tid;
-        };
-        auto fetch = [&](int tile) {
-            const int64_t t = t0 + (int64_t)tile * TT;
-            if (tile < tiles) {
+        auto next = [&](int slot) { return slot + 1 == NS ? 0 : slot + 1; };
+        const int64_t row_bytes = (int64_t)p.D * kElem, bc_bytes = (int64_t)p.G * p.n * kElem;
+        const int64_t at0 = ((t0 + row0) * p.D + c0 + col) * kElem;
+        int64_t fetch_at = at0, out_at = at0, bc_at = (t0 * p.G + g) * p.n * kElem;
+        int fetch_slot = 0, convert_slot = 0, out_slot = 0, fetch_t = 0, convert_t = 0, out_t = 0;
+        auto fetch = [&]() {
+            if (fetch_t < len) {
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    const int64_t tt = t + row_of(i), off = tt * p.D + c0 + col;
-                    const int on = on_of(i, tt);
-                    copy_four<BF16>(raw(tile, 3 * i), p.u, off, on, p.vec);
-                    copy_four<BF16>(raw(tile, 3 * i + 1), p.dt, off, on, p.vec);
-                    if (!SUMMARY && p.z) copy_four<BF16>(raw(tile, 3 * i + 2), p.z, off, on, p.vec);
+                    const int64_t off = fetch_at + i * kRowStep * row_bytes;
+                    const int on = on_of(i, fetch_t);
+                    copy_four<BF16>(raw(fetch_slot, 3 * i), p.u, static_cast<const char *>(p.u) + off, on, p.vec);
+                    copy_four<BF16>(raw(fetch_slot, 3 * i + 1), p.dt, static_cast<const char *>(p.dt) + off, on, p.vec);
+                    if (!SUMMARY && p.z) copy_four<BF16>(raw(fetch_slot, 3 * i + 2), p.z, static_cast<const char *>(p.z) + off, on, p.vec);
                 }
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
-                    const int i = tid + q * kStageThreads;   // row i / L, states 4 (i % L) ..
-                    const int64_t tb = t + i / L;
-                    const int mm = 4 * (i % L);
+                    const int i = tid + q * kStageThreads, mm = 4 * (i % L);   // row i / L, states 4 (i % L) ..
                     int v4 = p.n - mm;
-                    v4 = (i < TT * L && tb < t1 && v4 > 0) ? (v4 > 4 ? 4 : v4) : 0;
-                    copy_four<BF16>(&raw_bc(tile, q)->b, p.B, (tb * p.G + g) * p.n + mm, v4, p.vecn);
-                    if (!SUMMARY) copy_four<BF16>(&raw_bc(tile, q)->c, p.C, (tb * p.G + g) * p.n + mm, v4, p.vecn);
+                    v4 = (i < TT * L && fetch_t + i / L < len && v4 > 0) ? (v4 > 4 ? 4 : v4) : 0;
+                    const int64_t off = bc_at + (i / L) * bc_bytes + mm * kElem;
+                    copy_four<BF16>(&raw_bc(fetch_slot, q)->b, p.B, static_cast<const char *>(p.B) + off, v4, p.vecn);
+                    if (!SUMMARY) copy_four<BF16>(&raw_bc(fetch_slot, q)->c, p.C, static_cast<const char *>(p.C) + off, v4, p.vecn);
                 }
             }
             cp_async_commit();
+            fetch_at += TT * row_bytes;
+            bc_at += TT * bc_bytes;
+            fetch_t += TT;
+            fetch_slot = next(fetch_slot);
         };
-        auto convert = [&](int tile) {
-            const int64_t t = t0 + (int64_t)tile * TT;
-            float2 *d = buf_d(tile & 1);
+        auto convert = [&](int buf) {
+            float2 *d = buf_d(buf);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                if (row_of(i) >= TT) break;
-                const int on = on_of(i, t + row_of(i));
+                if (row0 + i * kRowStep >= TT) break;
+                const int on = on_of(i, convert_t);
                 float u[4], dt[4];
-                raw_four<BF16>(raw(tile, 3 * i), u);
-                raw_four<BF16>(raw(tile, 3 * i + 1), dt);
+                raw_four<BF16>(raw(convert_slot, 3 * i), u);
+                raw_four<BF16>(raw(convert_slot, 3 * i + 1), dt);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) dt[k] = on > k ? softplus(dt[k] + bias[k]) : 0.f;   // zero: the state passes unchanged
-                float4 *dst = reinterpret_cast<float4 *>(&d[row_of(i) * CH + col]);
+                float4 *dst = reinterpret_cast<float4 *>(&d[(row0 + i * kRowStep) * CH + col]);
                 dst[0] = make_float4(dt[0], dt[0] * u[0], dt[1], dt[1] * u[1]);
                 dst[1] = make_float4(dt[2], dt[2] * u[2], dt[3], dt[3] * u[3]);
             }
@@ -353,50 +385,54 @@ __global__ void __launch_bounds__(kScanThreads + kStageThreads, 1) scan_fwd_kern
             for (int q = 0; q < Q; ++q) {
                 const int i = tid + q * kStageThreads;
                 if (i < TT * L) {
-                    if constexpr (SUMMARY) buf_bc(tile & 1)[i].b = raw_bc(tile, q)->b;
-                    else buf_bc(tile & 1)[i] = *raw_bc(tile, q);
+                    if constexpr (SUMMARY) buf_bc(buf)[i].b = raw_bc(convert_slot, q)->b;
+                    else buf_bc(buf)[i] = *raw_bc(convert_slot, q);
                 }
             }
+            convert_t += TT;
+            convert_slot = next(convert_slot);
         };
-        auto write_out = [&](int tile) {
+        auto write_out = [&](int buf) {
             if constexpr (!SUMMARY) {
-                const int64_t t = t0 + (int64_t)tile * TT;
-                const float *y = buf_y(tile & 1);
+                const float *y = buf_y(buf);
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    const int64_t tt = t + row_of(i);
-                    const int on = on_of(i, tt);
+                    const int on = on_of(i, out_t);
                     if (on == 0) continue;
-                    const float4 yv = *reinterpret_cast<const float4 *>(&y[row_of(i) * YS + col]);
+                    const float4 yv = *reinterpret_cast<const float4 *>(&y[(row0 + i * kRowStep) * YS + col]);
                     float o[4] = {yv.x, yv.y, yv.z, yv.w}, r[4];
                     if (p.skip) {
-                        raw_four<BF16>(raw(tile, 3 * i), r);
+                        raw_four<BF16>(raw(out_slot, 3 * i), r);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) o[k] = fmaf(skip[k], r[k], o[k]);
                     }
                     if (p.z) {
-                        raw_four<BF16>(raw(tile, 3 * i + 2), r);
+                        raw_four<BF16>(raw(out_slot, 3 * i + 2), r);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) o[k] *= silu(r[k]);
                     }
-                    if (p.vec) store_piece<BF16, 4, true>(p.out, tt * p.D + c0 + col, on, o);
-                    else store_piece<BF16, 4, false>(p.out, tt * p.D + c0 + col, on, o);
+                    char *dst = static_cast<char *>(p.out) + out_at + i * kRowStep * row_bytes;
+                    if (p.vec) store_piece<BF16, 4, true>(dst, 0, on, o);
+                    else store_piece<BF16, 4, false>(dst, 0, on, o);
                 }
+                out_at += TT * row_bytes;
+                out_t += TT;
+                out_slot = next(out_slot);
             }
         };
-        for (int i = 0; i + 1 < NS; ++i) fetch(i);
+        for (int i = 0; i + 1 < NS; ++i) fetch();
         cp_async_wait_group<NS - 2>();
         if (tiles > 0) convert(0);
         __syncthreads();
-        for (int i = 0; i < tiles; ++i) {   // tile i is being scanned
-            if (i > 0) write_out(i - 1);    // the last use of that tile's slot
-            fetch(i - 1 + NS);
-            cp_async_wait_group<NS - 2>();  // tile i + 1 has landed
-            if (i + 1 < tiles) convert(i + 1);
+        for (int i = 0; i < tiles; ++i) {              // tile i is being scanned
+            if (i > 0) write_out((i - 1) & 1);         // the last use of that tile's slot
+            fetch();                                   // tile i - 1 + NS
+            cp_async_wait_group<NS - 2>();             // tile i + 1 has landed
+            if (i + 1 < tiles) convert((i + 1) & 1);
             __syncthreads();
         }
         cp_async_wait_all();
-        if (tiles > 0) write_out(tiles - 1);
+        if (tiles > 0) write_out((tiles - 1) & 1);
         return;
     }
 
