@@ -365,6 +365,16 @@ __global__ void __launch_bounds__(kConvThreads) conv_state_bwd_kernel(const Conv
         if (s0 == s1 && s0 < r0) continue;
         const int64_t p0 = s0 > r0 ? s0 : r0, p1 = min64(s1, r1);   // this run's tokens of the sequence
         if (p0 > p1 || (p0 == p1 && s0 != s1)) continue;
+        if (s0 == s1) {   // no tokens: the final state was the initial one
+            if (p.dh0)
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) {
+                    f32x2 e[N];
+                    cg.load_f32(p.dhN, (seq * (W - 1) + j) * p.C, p.dhN != nullptr, e);
+                    cg.store(p.dh0, (seq * (W - 1) + j) * p.C, e);
+                }
+            continue;
+        }
         // rows i = 0 .. from p0 on: own of them are this run's, with_data have tokens, end complete the inputs
         const int own = static_cast<int>(p1 - p0), end = own + W - 1, with_data = static_cast<int>(min64(end, s1 - p0));
         f32x2 xw[W > 1 ? W - 1 : 1][N], qw[W > 1 ? W - 1 : 1][N];   // inputs and gradients of the last W - 1 tokens

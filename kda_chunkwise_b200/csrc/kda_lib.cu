@@ -1425,8 +1425,10 @@ kda_status kda_selective_scan_fwd(const void *u, const void *dt, const float *A_
     p.num_seqs = num_seqs;
     p.D = D; p.n = n; p.G = G;
     p.seg_len = scan_segment_len(total_tokens, num_seqs, D, n, G);
-    p.vec = (D / G) % 4 == 0 && all_aligned({u, dt, z, out});
-    p.vecn = n % 4 == 0 && all_aligned({B, C, initial_state, final_state});
+    const bool act16 = all_aligned({u, dt, z, out}), bc16 = all_aligned({B, C});
+    p.unit = !act16 ? 1 : ((D / G) % 4 == 0 ? 4 : ((D / G) % 2 == 0 ? 2 : 1));
+    p.unit_n = !bc16 ? 1 : (n % 4 == 0 ? 4 : (n % 2 == 0 ? 2 : 1));
+    p.vecn = n % 4 == 0 && all_aligned({initial_state, final_state});
     p.cbg = scan_blocks_of_group(D, n, G, 1);
     const int64_t blocks = space.records * G * p.cbg;
     if (blocks > 0x7fffffffLL) return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_fwd: too many sequences and channels");

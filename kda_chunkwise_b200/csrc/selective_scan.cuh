@@ -53,8 +53,8 @@ struct ScanParams {
     int num_seqs, D, n, G;
     int cbg;                            // channel blocks of a group
     int64_t seg_len;
-    bool vec;                           // channels of u, dt, z and out may be moved in fours
-    bool vecn;                          // n is a multiple of four
+    int unit, unit_n;                   // channels (states of B and C) that may be moved at once: 4, 2 or 1
+    bool vecn;                          // states are moved in fours
     bool by_length;                     // blocks of long sequences first
 };
 
@@ -248,26 +248,38 @@ struct ScanSmem {
     static constexpr int kBytes = 2 * kBuf + kStages * kRaw;
 };
 
-// Asynchronous copy of four elements to shared memory, or zeros past `on` of them.  bf16 that may not be
-// moved as a vector is read and stored at once.
+// Asynchronous copy of four elements to shared memory, or zeros past `on` of them; `unit`: how many elements (4, 2
+// or 1) the addresses allow to be moved at once.  Single bf16 elements cannot be copied asynchronously: they are
+// read with read_four and stored with store_raw instead.
 template <bool BF16>
-__device__ __forceinline__ void copy_four(void *dst, const void *tensor, const char *at, int on, bool vec) {
-    constexpr int kElem = BF16 ? 2 : 4, kBytes = 4 * kElem;
+__device__ __forceinline__ void copy_four(void *dst, const void *tensor, const char *at, int on, int unit) {
+    constexpr int kElem = BF16 ? 2 : 4;
     const char *src = on > 0 ? at : static_cast<const char *>(tensor);   // (an address that may be named)
     const uint32_t to = smem_u32(dst);
-    if (vec) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(to), "l"(src), "n"(kBytes), "r"(on > 0 ? kBytes : 0) : "memory");
-    } else if constexpr (!BF16) {
+    if (unit == 4) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(to), "l"(src), "n"(4 * kElem), "r"(on > 0 ? 4 * kElem : 0) : "memory");
+    } else if (BF16 || unit == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(to + kElem * i), "l"(src + (on > i ? kElem * i : 0)),
+                         "n"(2 * kElem), "r"(on > i + 1 ? 2 * kElem : 0) : "memory");
+    } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(to + 4 * i), "l"(src + (on > i ? 4 * i : 0)), "r"(on > i ? 4 : 0) : "memory");
-    } else {
-        uint16_t v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = on > i ? reinterpret_cast<const uint16_t *>(src)[i] : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) static_cast<uint16_t *>(dst)[i] = v[i];
     }
+}
+
+__device__ __forceinline__ void read_four(const char *at, int on, uint32_t (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = 0u;
+        load_if<2, true>(at + 2 * i, on > i, &v[i]);
+    }
+}
+
+__device__ __forceinline__ void store_raw(void *dst, const uint32_t (&v)[4]) {
+    *static_cast<uint2 *>(dst) = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
 }
 
 template <bool BF16>
@@ -342,13 +354,26 @@ __global__ void __launch_bounds__(kScanThreads + kStageThreads, 1) scan_fwd_kern
         int fetch_slot = 0, convert_slot = 0, out_slot = 0, fetch_t = 0, convert_t = 0, out_t = 0;
         auto fetch = [&]() {
             if (fetch_t < len) {
+                if (BF16 && p.unit == 1) {   // all on their way before the first is waited for
+                    uint32_t r[3 * R][4];
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        const int64_t off = fetch_at + i * kRowStep * row_bytes;
+                        const int on = on_of(i, fetch_t);
+                        read_four(static_cast<const char *>(p.u) + off, on, r[3 * i]);
+                        read_four(static_cast<const char *>(p.dt) + off, on, r[3 * i + 1]);
+                        read_four(static_cast<const char *>(p.z) + off, !SUMMARY && p.z ? on : 0, r[3 * i + 2]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 3 * R; ++i) store_raw(raw(fetch_slot, i), r[i]);
+                } else
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     const int64_t off = fetch_at + i * kRowStep * row_bytes;
                     const int on = on_of(i, fetch_t);
-                    copy_four<BF16>(raw(fetch_slot, 3 * i), p.u, static_cast<const char *>(p.u) + off, on, p.vec);
-                    copy_four<BF16>(raw(fetch_slot, 3 * i + 1), p.dt, static_cast<const char *>(p.dt) + off, on, p.vec);
-                    if (!SUMMARY && p.z) copy_four<BF16>(raw(fetch_slot, 3 * i + 2), p.z, static_cast<const char *>(p.z) + off, on, p.vec);
+                    copy_four<BF16>(raw(fetch_slot, 3 * i), p.u, static_cast<const char *>(p.u) + off, on, p.unit);
+                    copy_four<BF16>(raw(fetch_slot, 3 * i + 1), p.dt, static_cast<const char *>(p.dt) + off, on, p.unit);
+                    if (!SUMMARY && p.z) copy_four<BF16>(raw(fetch_slot, 3 * i + 2), p.z, static_cast<const char *>(p.z) + off, on, p.unit);
                 }
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
@@ -356,8 +381,17 @@ __global__ void __launch_bounds__(kScanThreads + kStageThreads, 1) scan_fwd_kern
                     int v4 = p.n - mm;
                     v4 = (i < TT * L && fetch_t + i / L < len && v4 > 0) ? (v4 > 4 ? 4 : v4) : 0;
                     const int64_t off = bc_at + (i / L) * bc_bytes + mm * kElem;
-                    copy_four<BF16>(&raw_bc(fetch_slot, q)->b, p.B, static_cast<const char *>(p.B) + off, v4, p.vecn);
-                    if (!SUMMARY) copy_four<BF16>(&raw_bc(fetch_slot, q)->c, p.C, static_cast<const char *>(p.C) + off, v4, p.vecn);
+                    const char *b = static_cast<const char *>(p.B) + off, *c = static_cast<const char *>(p.C) + off;
+                    if (BF16 && p.unit_n == 1) {
+                        uint32_t r[2][4];
+                        read_four(b, v4, r[0]);
+                        read_four(c, SUMMARY ? 0 : v4, r[1]);
+                        store_raw(&raw_bc(fetch_slot, q)->b, r[0]);
+                        store_raw(&raw_bc(fetch_slot, q)->c, r[1]);
+                    } else {
+                        copy_four<BF16>(&raw_bc(fetch_slot, q)->b, p.B, b, v4, p.unit_n);
+                        if (!SUMMARY) copy_four<BF16>(&raw_bc(fetch_slot, q)->c, p.C, c, v4, p.unit_n);
+                    }
                 }
             }
             cp_async_commit();
@@ -412,8 +446,15 @@ __global__ void __launch_bounds__(kScanThreads + kStageThreads, 1) scan_fwd_kern
                         for (int k = 0; k < 4; ++k) o[k] *= silu(r[k]);
                     }
                     char *dst = static_cast<char *>(p.out) + out_at + i * kRowStep * row_bytes;
-                    if (p.vec) store_piece<BF16, 4, true>(dst, 0, on, o);
-                    else store_piece<BF16, 4, false>(dst, 0, on, o);
+                    if (p.unit == 4) {
+                        store_piece<BF16, 4, true>(dst, 0, on, o);
+                    } else if (p.unit == 2) {
+                        const float lo[2] = {o[0], o[1]}, hi[2] = {o[2], o[3]};
+                        store_piece<BF16, 2, true>(dst, 0, on, lo);
+                        store_piece<BF16, 2, true>(dst, 2, on - 2, hi);
+                    } else {
+                        store_piece<BF16, 4, false>(dst, 0, on, o);
+                    }
                 }
                 out_at += TT * row_bytes;
                 out_t += TT;

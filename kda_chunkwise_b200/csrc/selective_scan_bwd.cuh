@@ -79,7 +79,9 @@ __device__ __forceinline__ void stage_bwd(const ScanBwdParams &p, const ScanBwdP
                                           float *s_dy, QuadBC<BF16> *s_bc) {
     using Tile = ScanBwdTile<L>;
     constexpr int YS = Tile::kYS, R = Tile::kR, AHEAD = R < 4 ? R : 4;
-    for (int i = threadIdx.x; i < Tile::kTC * L; i += kScanThreads) {   // row i / L, states 4 (i % L) ..
+    // rows up to the end of the last kBack tokens that hold any
+    const int rows = (static_cast<int>(at.t1 - at.t0) + Tile::kBack - 1) / Tile::kBack * Tile::kBack;
+    for (int i = threadIdx.x; i < rows * L; i += kScanThreads) {   // row i / L, states 4 (i % L) ..
         const int64_t tb = at.t0 + i / L;
         const int mm = 4 * (i % L);
         int v4 = p.n - mm;
@@ -94,7 +96,7 @@ __device__ __forceinline__ void stage_bwd(const ScanBwdParams &p, const ScanBwdP
 #pragma unroll
     for (int k = 0; k < 4; ++k) bias[k] = p.dt_bias && at.left > at.col() + k ? p.dt_bias[at.c0 + at.col() + k] : 0.f;
 #pragma unroll 1
-    for (int i0 = 0; i0 < R; i0 += AHEAD) {
+    for (int i0 = 0; i0 * (kScanThreads / Tile::kFR) < rows; i0 += AHEAD) {
         Piece<BF16, 4> ru[AHEAD], rdt[AHEAD], rdo[AHEAD], rz[AHEAD];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(kScanThreads, L > 4 ? 2 : 3) scan_bwd_grad_ker
     ScanBwdPlace<L> at;
     at.c0 = (int64_t)g * DG + cbase;
     at.left = DG - cbase;
-    const bool chunk = scan_segment(p.cu, p.num_seqs, p.total_tokens, TC, rec, seq, j, at.t0, at.t1, last);
+    const bool chunk = scan_segment(p.cu, p.num_seqs, p.total_tokens, TC, rec, seq, j, at.t0, at.t1, last) && at.t0 < at.t1;
     f32x2 h01[KC], h23[KC], g01[KC], g23[KC];   // g: a_{t+1} g_{t+1}
     float A2[KC][4];
     f32x2 dA01[KC], dA23[KC];
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kScanThreads, L > 4 ? 2 : 3) scan_bwd_grad_ker
         const bool active = chl + k * Tile::kStep < at.left;
         const int64_t c = at.c0 + chl + k * Tile::kStep, row = (rec * p.D + c) * p.n;
         float h[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f};
-        if (!chunk) {   // a record without a chunk: nothing to the weights' sums
+        if (!chunk) {   // a record without tokens: nothing to the weights' sums
             if (active) {
                 store_quad(p.H + row, m0, p.n, p.vecn, h);
                 if (lane == 0) p.pskip[rec * p.D + c] = p.pbias[rec * p.D + c] = 0.f;
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(kScanThreads, L > 4 ? 2 : 3) scan_bwd_grad_ker
         }
     }
 #pragma unroll 2
-    for (int i = 0; i < Tile::kR; ++i) {
+    for (int i = 0; i < Tile::kR && i * (kScanThreads / Tile::kFR) < tokens; ++i) {
         const int on = at.on(i), x = at.row(i) * YS + at.col();
         const int64_t off = at.off(i, p.D);
         Piece<BF16, 4> rz, rdo;
