@@ -1333,16 +1333,26 @@ ScanSpace scan_space(int64_t T, int32_t num_seqs, int32_t D, int32_t n, int32_t 
     return s;
 }
 
+template <bool BF16, int L, int ST, bool SUMMARY>
+kda_status launch_scan_pass(const kda::ScanParams &p, int64_t blocks, cudaStream_t s) {
+    constexpr int smem = kda::ScanSmem<BF16, L, ST>::kBytes;
+    auto kernel = kda::scan_fwd_kernel<BF16, L, ST, SUMMARY>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(selective_scan_fwd)");
+    kernel<<<(unsigned)blocks, kda::kScanThreads + ST, smem, s>>>(p);
+    return launched("selective_scan_fwd launch");
+}
+
+// Two blocks an SM with half the staging threads where there are blocks for it; one block with all of them
+// otherwise (SCAN_BOTH).
 template <bool BF16, int L>
 kda_status launch_scan_fwd(const kda::ScanParams &p, int64_t blocks, bool cut, cudaStream_t s) {
-    constexpr int smem = kda::ScanSmem<BF16, L>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(kda::scan_fwd_kernel<BF16, L, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && cut)
-        e = cudaFuncSetAttribute(kda::scan_fwd_kernel<BF16, L, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(selective_scan_fwd)");
-    if (cut) kda::scan_fwd_kernel<BF16, L, true><<<(unsigned)blocks, kda::kScanThreads + kda::kStageThreads, smem, s>>>(p);
-    kda::scan_fwd_kernel<BF16, L, false><<<(unsigned)blocks, kda::kScanThreads + kda::kStageThreads, smem, s>>>(p);
-    return launched("selective_scan_fwd launch", cut ? 2 : 1);
+    if (cut) {
+        const kda_status st = launch_scan_pass<BF16, L, 256, true>(p, blocks, s);
+        if (st != KDA_OK) return st;
+    }
+    return blocks >= 2 * (int64_t)device_sm_count() ? launch_scan_pass<BF16, L, 128, false>(p, blocks, s)
+                                                    : launch_scan_pass<BF16, L, 256, false>(p, blocks, s);
 }
 
 // the checks that the scan's entry points share; `where` names the entry point
@@ -1433,7 +1443,8 @@ kda_status kda_selective_scan_fwd(const void *u, const void *dt, const float *A_
     const int64_t blocks = space.records * G * p.cbg;
     if (blocks > 0x7fffffffLL) return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_fwd: too many sequences and channels");
     const bool cut = space.total > 0;
-    p.by_length = !cut && num_seqs > 1 && num_seqs <= kda::kRankSeqs && blocks > device_sm_count();
+    p.by_length = !cut && num_seqs > 1 && num_seqs <= kda::kRankSeqs && blocks > device_sm_count() &&
+                  total_tokens >= (int64_t)128 * num_seqs;   // (short ones end before the order is found)
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return with_dtype(dtype, [&](auto bf16) {
         return with_lanes(n, [&](auto lanes) {

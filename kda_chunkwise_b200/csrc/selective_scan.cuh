@@ -11,7 +11,7 @@
 // channel) (softplus, the gate) is done once, not once per state.
 //   - A channel's n states lie on L = 2^ceil(log2(n / 4)) lanes, four to a lane; 128 threads scan
 //     KC x 128 / L channels of one group over one segment of one sequence.
-//   - 256 more threads stage the next tile of tokens and write the outputs of the last one meanwhile, so
+//   - 256 more threads (128 where two blocks share an SM) stage the next tile of tokens and write the outputs of the last one meanwhile, so
 //     that the scanning warps only scan: with one sequence there is about one of them per scheduler.
 //   - What a scanning thread reads from shared memory per token is the next bound: B and C lie next to
 //     each other, in bf16 where they came in bf16, and serve the KC channels of a thread.
@@ -26,16 +26,16 @@
 
 namespace kda {
 
-constexpr int kScanThreads = 128;    // that scan
-constexpr int kStageThreads = 256;   // that stage for them
+constexpr int kScanThreads = 128;   // that scan
 
-template <int L>
+// ST: threads that stage for them
+template <int L, int ST>
 struct ScanTile {
     static constexpr int kCH = kScanThreads / L;             // channels of a block
     static constexpr int kTT = L >= 4 ? 64 : 16 * L;         // tokens of a tile
     static constexpr int kFR = kCH / 4;                      // fours of channels of a row
-    static constexpr int kR = (kTT * kFR + kStageThreads - 1) / kStageThreads;   // of them a staging thread holds
-    static constexpr int kQ = (kTT * L + kStageThreads - 1) / kStageThreads;     // fours of states of B (and C) it holds
+    static constexpr int kR = (kTT * kFR + ST - 1) / ST;           // of them a staging thread holds
+    static constexpr int kQ = (kTT * L + ST - 1) / ST;             // fours of states of B (and C) it holds
     static constexpr int kYS = kCH + (L == 16 ? 4 : 32 / L); // row stride of outputs: the lanes' rows fall on different banks
 };
 
@@ -63,7 +63,8 @@ struct ScanParams {
 __device__ __forceinline__ bool scan_segment(const int32_t *cu, int num_seqs, int64_t total, int64_t seg_len, int64_t rec,
                                              int &seq, int64_t &j, int64_t &t0, int64_t &t1, bool &last) {
     int lo = 0, hi = num_seqs;
-    while (hi - lo > 1) {
+    if (seg_len > total) lo = static_cast<int>(rec);   // uncut: a record is a sequence
+    else while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         int64_t c = cu[mid];
         c = c < 0 ? 0 : (c > total ? total : c);
@@ -235,15 +236,15 @@ __device__ __forceinline__ void decays(const float (&A2)[4], float delta, f32x2 
     a23 = f2_pack(ex2_approx(A2[2] * delta), ex2_approx(A2[3] * delta));
 }
 
-template <bool BF16, int L>
+template <bool BF16, int L, int ST>
 struct ScanSmem {
-    using Tile = ScanTile<L>;
+    using Tile = ScanTile<L, ST>;
     static constexpr int kD = Tile::kTT * Tile::kCH;       // float2 (delta, delta u)
     static constexpr int kBC = Tile::kTT * L;              // QuadBC
     static constexpr int kY = Tile::kTT * Tile::kYS;       // float
     static constexpr int kBuf = kD * 8 + kBC * (int)sizeof(QuadBC<BF16>) + kY * 4;   // of one tile being scanned
     static constexpr int kFour = BF16 ? 8 : 16;            // bytes of four raw elements
-    static constexpr int kRaw = kStageThreads * (3 * Tile::kR * kFour + Tile::kQ * (int)sizeof(QuadBC<BF16>));   // of one tile on its way
+    static constexpr int kRaw = ST * (3 * Tile::kR * kFour + Tile::kQ * (int)sizeof(QuadBC<BF16>));   // of one tile on its way
     static constexpr int kStages = 3;
     static constexpr int kBytes = 2 * kBuf + kStages * kRaw;
 };
@@ -296,13 +297,13 @@ __device__ __forceinline__ void raw_four(const void *p, float (&v)[4]) {
     }
 }
 
-// Threads 0 .. 127 scan, 128 .. 383 stage; one barrier a tile.  While tile i is scanned, the outputs of tile i - 1
+// Threads 0 .. 127 scan, ST more stage; one barrier a tile.  While tile i is scanned, the outputs of tile i - 1
 // are written, tile i + 1 is converted and the tiles after it are on their way into a ring (every
 // staging thread reads back what it copied itself).
-template <bool BF16, int L, bool SUMMARY>
-__global__ void __launch_bounds__(kScanThreads + kStageThreads, 1) scan_fwd_kernel(const ScanParams p) {
-    using Tile = ScanTile<L>;
-    using SM = ScanSmem<BF16, L>;
+template <bool BF16, int L, int ST, bool SUMMARY>
+__global__ void __launch_bounds__(kScanThreads + ST, ST == 128 ? 2 : 1) scan_fwd_kernel(const ScanParams p) {
+    using Tile = ScanTile<L, ST>;
+    using SM = ScanSmem<BF16, L, ST>;
     constexpr int CH = Tile::kCH, TT = Tile::kTT, R = Tile::kR, Q = Tile::kQ, YS = Tile::kYS, FR = Tile::kFR, NS = SM::kStages;
     extern __shared__ __align__(16) unsigned char scan_tiles[];
     auto buf_bc = [&](int b) { return reinterpret_cast<QuadBC<BF16> *>(scan_tiles + b * SM::kBuf); };
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kScanThreads + kStageThreads, 1) scan_fwd_kern
         const int tid = threadIdx.x - kScanThreads;
         // four i of this thread: row row0 + i kRowStep of a tile (past it where there are more threads than
         // fours), and the channels within the block, the same for every i
-        constexpr int kElem = BF16 ? 2 : 4, kRowStep = kStageThreads / FR;
+        constexpr int kElem = BF16 ? 2 : 4, kRowStep = ST / FR;
         const int row0 = tid / FR, col = 4 * (tid % FR), left = DG - cbase - col, four_on = left > 0 ? (left > 4 ? 4 : left) : 0;
         const int len = static_cast<int>(t1 - t0);
         // how many channels of four i exist in the tile whose first token is t0 + t
@@ -342,10 +343,10 @@ __global__ void __launch_bounds__(kScanThreads + kStageThreads, 1) scan_fwd_kern
         // This thread's part of a ring slot: fours of u, dt and z, and of B and C.  Offsets (in bytes of global memory,
         // in slots of the ring) move along with the tiles.
         unsigned char *const ring = scan_tiles + 2 * SM::kBuf + tid * SM::kFour;
-        auto raw = [&](int slot, int which) { return ring + slot * SM::kRaw + which * (kStageThreads * SM::kFour); };
-        unsigned char *const ring_bc = scan_tiles + 2 * SM::kBuf + 3 * R * kStageThreads * SM::kFour + tid * sizeof(QuadBC<BF16>);
+        auto raw = [&](int slot, int which) { return ring + slot * SM::kRaw + which * (ST * SM::kFour); };
+        unsigned char *const ring_bc = scan_tiles + 2 * SM::kBuf + 3 * R * ST * SM::kFour + tid * sizeof(QuadBC<BF16>);
         auto raw_bc = [&](int slot, int q) {
-            return reinterpret_cast<QuadBC<BF16> *>(ring_bc + slot * SM::kRaw + q * (kStageThreads * sizeof(QuadBC<BF16>)));
+            return reinterpret_cast<QuadBC<BF16> *>(ring_bc + slot * SM::kRaw + q * (ST * sizeof(QuadBC<BF16>)));
         };
         auto next = [&](int slot) { return slot + 1 == NS ? 0 : slot + 1; };
         const int64_t row_bytes = (int64_t)p.D * kElem, bc_bytes = (int64_t)p.G * p.n * kElem;
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(kScanThreads + kStageThreads, 1) scan_fwd_kern
                 }
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
-                    const int i = tid + q * kStageThreads, mm = 4 * (i % L);   // row i / L, states 4 (i % L) ..
+                    const int i = tid + q * ST, mm = 4 * (i % L);   // row i / L, states 4 (i % L) ..
                     int v4 = p.n - mm;
                     v4 = (i < TT * L && fetch_t + i / L < len && v4 > 0) ? (v4 > 4 ? 4 : v4) : 0;
                     const int64_t off = bc_at + (i / L) * bc_bytes + mm * kElem;
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kScanThreads + kStageThreads, 1) scan_fwd_kern
             }
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                const int i = tid + q * kStageThreads;
+                const int i = tid + q * ST;
                 if (i < TT * L) {
                     if constexpr (SUMMARY) buf_bc(buf)[i].b = raw_bc(convert_slot, q)->b;
                     else buf_bc(buf)[i] = *raw_bc(convert_slot, q);
