@@ -96,7 +96,7 @@ def check_scan(kda, lens, v, out, last):
 
 SHAPES = [  # D, G, n: every number of lanes, states that fill no quad, channels that fill no vector or block
     (1, 1, 1), (7, 1, 3), (40, 1, 4), (128, 1, 5), (130, 2, 8), (33, 3, 11), (64, 1, 16), (40, 4, 16), (100, 1, 16),
-    (24, 2, 17), (16, 1, 32), (9, 1, 33), (24, 3, 64), (256, 1, 16),
+    (24, 2, 17), (16, 1, 32), (9, 1, 33), (24, 3, 64), (256, 1, 16), (20, 2, 6), (12, 1, 18), (36, 1, 2),
 ]
 LENS = [[1], [5, 0, 33, 1, 0], [31, 32, 64, 65]]
 
@@ -139,6 +139,73 @@ def test_scan_forward_cut_into_segments(kda, lens, D, G, n):
     pool = v["h0"].clone()
     out2, last2 = kda.kda_selective_scan_fwd(*args, cu, **{**kw, "initial_state": pool}, final_state=pool)
     assert last2 is pool and torch.equal(last2, last) and torch.equal(out2, out)
+
+
+@pytest.mark.parametrize("D", [2048, 4096])
+def test_scan_forward_more_blocks_than_the_gpu_holds(kda, D):
+    """Blocks of long sequences start first; from twice the SMs on, two blocks share one."""
+    lens, n = [200, 500, 0, 300], 16
+    assert kda.kda_selective_scan_fwd_workspace_size(sum(lens), len(lens), D, n, 2) == 0
+    v = scan_inputs(lens, D, 2, n, BF)
+    args, kw = call_args(v)
+    out, last = kda.kda_selective_scan_fwd(*args, dev_cu(lens), **kw)
+    check_scan(kda, lens, v, out, last)
+
+
+def test_many_short_sequences(kda):
+    """Hundreds of sequences of none to five tokens: several to a run, to a tile, to a chunk's rows."""
+    r = np.random.default_rng(0)
+    lens = [int(x) for x in r.integers(0, 6, size=300)]
+    cu = dev_cu(lens)
+    for t, D, n in ((BF, 40, 16), (F32, 7, 3)):
+        v = scan_inputs(lens, D, 1, n, t)
+        args, kw = call_args(v)
+        out, last = kda.kda_selective_scan_fwd(*args, cu, **kw)
+        check_scan(kda, lens, v, out, last)
+        dout = torch.randn(sum(lens), D, generator=gen(1), device="cuda").to(t)
+        dlast = torch.randn(len(lens), D, n, generator=gen(2), device="cuda")
+        check_scan_grads(lens, v, dout, dlast, kda.kda_selective_scan_bwd(*args, cu, dout, dfinal_state=dlast, **kw))
+        x = conv_inputs(lens, 1, D, 4, t, True, True)
+        ckw = dict(bias=x["bias"], initial_state=x["h0"], silu=True)
+        y, window = kda.kda_short_conv_fwd(x["x"], x["w"], cu, **ckw)
+        dy = torch.randn(y.shape, generator=gen(3), device="cuda").to(t)
+        dw = torch.randn(window.shape, generator=gen(4), device="cuda").to(t)
+        got = kda.kda_short_conv_bwd(x["x"], x["w"], cu, dy, dfinal_state=dw, **ckw)
+        ry, rwin, ys, rg, scale = conv_refs(lens, x, True, False, dy, dw)
+        check("y", y, ry, ys, 2.0 ** -20)
+        assert np.array_equal(host(window), rwin)
+        for k in rg:
+            check(k, got[k], rg[k], scale[k], 2.0 ** -19 + (sum(lens) * 2.0 ** -24 if k in ("dw", "dbias") else 0.0))
+
+
+def test_caller_s_workspaces(kda):
+    """Workspaces of the caller's, of exactly the size asked for and holding anything, give the same bits; smaller
+    ones are refused."""
+    lens, D, n = [600, 200], 40, 16
+    v = scan_inputs(lens, D, 1, n, BF)
+    args, kw = call_args(v)
+    cu = dev_cu(lens)
+    dout = torch.randn(800, D, generator=gen(1), device="cuda").to(BF)
+    x = conv_inputs(lens, 1, 40, 4, BF, True, True)
+    rows = x["x"].view(800, 40)
+    w = torch.randn(40, generator=gen(2), device="cuda")
+    _, mean, rstd = kda.kda_layer_norm_fwd(rows, w)
+    calls = [
+        (kda.kda_selective_scan_fwd_workspace_size(800, 2, D, n), lambda **s: kda.kda_selective_scan_fwd(*args, cu, **kw, **s)),
+        (kda.kda_selective_scan_bwd_workspace_size(800, 2, D, n), lambda **s: kda.kda_selective_scan_bwd(*args, cu, dout, **kw, **s)),
+        (kda.kda_short_conv_bwd_workspace_size(800, 1, 40, 4),
+         lambda **s: kda.kda_short_conv_bwd(x["x"], x["w"], cu, x["x"], bias=x["bias"], initial_state=x["h0"], **s)),
+        (kda.kda_layer_norm_bwd_workspace_size(800, 40), lambda **s: kda.kda_layer_norm_bwd(rows, w, mean, rstd, rows, **s)),
+    ]
+    values = lambda r: [t for t in (r.values() if isinstance(r, dict) else r) if t is not None]  # noqa: E731
+    for size, call in calls:
+        assert size > 0
+        ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")   # NaN in fp32
+        for a, b in zip(values(call()), values(call(workspace=ws))):
+            assert torch.equal(a, b)
+        with pytest.raises(kda.KDAError) as e:
+            call(workspace=ws[:size - 16])
+        assert e.value.status == kda.KDA_ERR_INVALID_ARG
 
 
 def test_scan_forward_state_in_place_uncut(kda):
