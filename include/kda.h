@@ -350,7 +350,8 @@ KDA_API size_t kda_chunk_bwd_workspace_size(int64_t total_tokens, int32_t num_se
  * The operators of a state-space layer, from here to kda_layer_norm_bwd (no counterpart in the pages):
  * scan, short convolution and norm, for prompts, single tokens and gradients.  Their activations and
  * states need only their own type's alignment; where all of a call's are 16-byte aligned and rows hold
- * whole vectors, they are moved as vectors.  Workspaces are 16-byte aligned.
+ * whole vectors, they are moved as vectors.  Workspaces are 16-byte aligned.  At most 2,147,418,112 tokens
+ * a call.
  *
  * Selective state space scan: the recurrence of a state-space layer, beside the gated delta rule.  Per channel c of D with n states, in group g = c / (D / G):
  *   delta_t = softplus(dt_t + dt_bias),  A = -exp(A_log)
@@ -399,8 +400,9 @@ KDA_API kda_status kda_selective_scan_step(const void *u, const void *dt, const 
  *   when z is given; dA_log fp32 [D, n]; dskip, ddt_bias fp32 [D], each may be NULL (not written);
  *   dinitial_state fp32 [num_seqs, D, n] or NULL.  All are overwritten; no output overlaps an input or
  *   another output.
- *   workspace: kda_selective_scan_bwd_workspace_size(...) bytes, 16-byte aligned, no initialisation: two states of
- *   every chunk of 16 ceil(n / 4) tokens (a power of two from 16 to 64) and the channel blocks' shares of dB and dC.
+ *   workspace: kda_selective_scan_bwd_workspace_size(...) bytes, 16-byte aligned, no initialisation: two states
+ *   [D, n] of every chunk (16 tokens up to n = 4, 32 up to 16, 64 beyond) and, for every block of channels (64 at
+ *   n = 16), its shares of dB and dC [total_tokens, 2 n]: 214 MB for 8192 tokens, D = 4096, n = 16, G = 1.
  * Deterministic.
  */
 KDA_API kda_status kda_selective_scan_bwd(const void *u, const void *dt, const float *A_log, const void *B,

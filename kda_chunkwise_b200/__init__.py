@@ -964,6 +964,7 @@ class _SelectiveScan(torch.autograd.Function):
         return out, last
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dout, dlast):
         u, dt, A_log, B, C, skip, z, dt_bias, initial_state, cu_seqlens = ctx.saved_tensors
         g = kda_selective_scan_bwd(u, dt, A_log, B, C, cu_seqlens, _grad(dout, u), skip=skip, z=z, dt_bias=dt_bias,
@@ -988,6 +989,7 @@ class _ShortConv(torch.autograd.Function):
         return y, last
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dlast):
         x, w, bias, initial_state, cu_seqlens = ctx.saved_tensors
         g = kda_short_conv_bwd(x, w, cu_seqlens, _grad(dy, x), bias=bias, initial_state=initial_state,
@@ -1010,6 +1012,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, w, mean, rstd = ctx.saved_tensors
         g = kda_layer_norm_bwd(x, w, mean, rstd, _grad(dy, x), has_bias=ctx.has_bias)

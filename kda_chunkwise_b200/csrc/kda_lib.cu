@@ -1296,8 +1296,10 @@ int scan_channels(int n, int KC) { return KC * (kda::kScanThreads / scan_lanes(n
 int scan_blocks_of_group(int D, int n, int G, int KC) { return (D / G + scan_channels(n, KC) - 1) / scan_channels(n, KC); }
 int scan_bwd_chunk(int n) { const int L = scan_lanes(n); return L > 4 ? 64 : (L == 4 ? 32 : 16 * L); }   // ScanBwdTile::kTC
 
+constexpr int64_t kMaxTokens = 0x7fff0000LL;   // token counts stay 32-bit a few tiles past the end
+
 bool scan_sizes_ok(int64_t rows, int32_t seqs, int32_t D, int32_t n, int32_t G) {
-    return rows >= 0 && rows <= 0x7fffffffLL && seqs >= 0 && D > 0 && n > 0 && G > 0 && D % G == 0;
+    return rows >= 0 && rows <= kMaxTokens && seqs >= 0 && D > 0 && n > 0 && G > 0 && D % G == 0;
 }
 
 // Tokens of a segment of the prompt's scan; more than total_tokens where sequences are not cut (so that
@@ -1416,7 +1418,8 @@ kda_status kda_selective_scan_fwd(const void *u, const void *dt, const float *A_
     if (initial_state != final_state && overlap(initial_state, state_bytes, final_state, state_bytes))
         return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_fwd: final_state overlaps initial_state in part");
     const size_t act = (size_t)total_tokens * D * elem_size(dtype), bc = (size_t)total_tokens * G * n * elem_size(dtype);
-    st = apart_check(where, {{out, act}}, {{u, act}, {dt, act}, {z, act}, {B, bc}, {C, bc}});
+    st = apart_check(where, {{out, act}, {final_state, state_bytes}}, {{u, act}, {dt, act}, {z, act}, {B, bc}, {C, bc}});
+    if (st == KDA_OK) st = apart_check(where, {{out, act}}, {{initial_state, state_bytes}, {final_state, state_bytes}});
     if (st != KDA_OK) return st;
     const ScanSpace space = scan_space(total_tokens, num_seqs, D, n, G);
     st = space_check(where, workspace, workspace_bytes, space.total * 4);
@@ -1466,7 +1469,9 @@ kda_status kda_selective_scan_step(const void *u, const void *dt, const float *A
     st = aligned_check(where, elem_size(dtype), {u, dt, B, C, z, out}, {A_log, skip, dt_bias, state});
     if (st != KDA_OK) return st;
     const size_t act = (size_t)N * D * elem_size(dtype), bc = (size_t)N * G * n * elem_size(dtype);
-    st = apart_check(where, {{out, act}, {state, (size_t)N * D * n * 4}}, {{u, act}, {dt, act}, {z, act}, {B, bc}, {C, bc}});
+    const Span st_span{state, (size_t)N * D * n * 4};
+    st = apart_check(where, {{out, act}, st_span}, {{u, act}, {dt, act}, {z, act}, {B, bc}, {C, bc}});
+    if (st == KDA_OK) st = apart_check(where, {{out, act}}, {st_span});
     if (st != KDA_OK) return st;
     kda::ScanStepParams p{};
     p.u = u; p.dt = dt; p.z = z; p.B = B; p.C = C;
@@ -1623,7 +1628,7 @@ int64_t conv_bwd_runs(int64_t T, int64_t C) {
 }
 
 bool conv_sizes_ok(int64_t rows, int32_t seqs, int32_t H, int32_t d) {
-    return rows >= 0 && rows <= 0x7fffffffLL && seqs >= 0 && H > 0 && d > 0 && (int64_t)H * d <= 0x1000000LL;
+    return rows >= 0 && rows <= kMaxTokens && seqs >= 0 && H > 0 && d > 0 && (int64_t)H * d <= 0x1000000LL;
 }
 
 kda_status conv_check(const char *where, int64_t rows, int32_t seqs, int32_t H, int32_t d, int32_t width, int32_t l2norm,
@@ -1665,7 +1670,8 @@ kda_status kda_short_conv_fwd(const void *x, const float *w, const float *bias, 
     const int64_t C = (int64_t)H * d;
     const size_t es = elem_size(dtype), rows_bytes = (size_t)total_tokens * C * es;
     const size_t state_bytes = (size_t)num_seqs * (width - 1) * C * es;
-    st = apart_check(where, {{y, rows_bytes}}, {{x, rows_bytes}});
+    st = apart_check(where, {{y, rows_bytes}, {final_state, state_bytes}}, {{x, rows_bytes}});
+    if (st == KDA_OK) st = apart_check(where, {{y, rows_bytes}}, {{initial_state, state_bytes}, {final_state, state_bytes}});
     if (st != KDA_OK) return st;
     if (initial_state != final_state && overlap(initial_state, state_bytes, final_state, state_bytes))
         return fail(KDA_ERR_INVALID_ARG, "kda_short_conv_fwd: final_state overlaps initial_state in part");
@@ -1720,7 +1726,9 @@ kda_status kda_short_conv_step(const void *x, const float *w, const float *bias,
     if (st != KDA_OK) return st;
     const int64_t C = (int64_t)H * d;
     const size_t rows_bytes = (size_t)N * C * elem_size(dtype);
-    st = apart_check(where, {{y, rows_bytes}, {state, rows_bytes * (width - 1)}}, {{x, rows_bytes}});
+    const Span st_span{state, rows_bytes * (width - 1)};
+    st = apart_check(where, {{y, rows_bytes}, st_span}, {{x, rows_bytes}});
+    if (st == KDA_OK) st = apart_check(where, {{y, rows_bytes}}, {st_span});
     if (st != KDA_OK) return st;
     kda::ConvStateParams p{};
     p.x = x; p.w = w; p.bias = bias;

@@ -126,11 +126,15 @@ __device__ __forceinline__ void store_quad(float *row, int m0, int n, bool vecn,
     }
 }
 
-// A log2(e) of N states; zero past n (a decay of one on states that stay zero)
+// A log2(e) of N states; zero past n (a decay of one on states that stay zero).  Finite, so that the tokens past a
+// sequence's end (delta = 0) leave the state as it is whatever A is; a NaN stays one.
 template <int N>
 __device__ __forceinline__ void load_decay(const float *A_log, int64_t c, int m0, int n, bool active, float (&A2)[N]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) A2[i] = active && m0 + i < n ? -1.4426950408889634f * expf(A_log[c * n + m0 + i]) : 0.f;
+    for (int i = 0; i < N; ++i) {
+        const float a = active && m0 + i < n ? -1.4426950408889634f * expf(A_log[c * n + m0 + i]) : 0.f;
+        A2[i] = a < -3e38f ? -3e38f : a;
+    }
 }
 
 __device__ __forceinline__ float silu(float x) { return x * sigmoid_fast(x); }

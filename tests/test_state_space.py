@@ -178,6 +178,9 @@ REFUSED = [
     (scan_fwd, dict(ws=_off(7, 8), T=4096), INVALID), (scan_fwd, dict(A_log=_off(2, 2)), INVALID),
     (scan_fwd, dict(out=_off(0, 64)), INVALID), (scan_fwd, dict(h0=_p(8), hN=_off(8, 16)), INVALID),
     (scan_fwd, dict(T=4096, ws_bytes=16), INVALID), (scan_fwd, dict(T=4096, ws=None), INVALID),
+    (scan_fwd, dict(T=(1 << 31) - 1), INVALID), (scan_fwd, dict(hN=_p(0)), INVALID), (scan_fwd, dict(out=_p(8), h0=_p(8), hN=_p(8)), INVALID),
+    (scan_step, dict(out=_p(5)), INVALID), (conv_fwd, dict(T=(1 << 31) - 1), INVALID), (conv_fwd, dict(hN=_p(3)), INVALID),
+    (conv_step, dict(state=_p(3)), INVALID),
     (scan_step, dict(n=65), UNSUPPORTED), (scan_step, dict(N=-1), INVALID), (scan_step, dict(G=3), INVALID),
     (scan_step, dict(state=None), INVALID), (scan_step, dict(dtype=-1), INVALID), (scan_step, dict(out=_p(0)), INVALID),
     (scan_step, dict(state=_off(5, 2)), INVALID), (scan_step, dict(state=_p(3)), INVALID),

@@ -302,6 +302,47 @@ def test_scan_decays_at_both_ends(kda):
         check_scan_grads(lens, v, dout, dlast, kda.kda_selective_scan_bwd(*args, dev_cu(lens), dout, dfinal_state=dlast, **kw))
 
 
+def test_scan_decay_past_the_largest_float(kda):
+    """A = -exp(A_log) past the largest fp32 value: the state is forgotten at once, also in a tile's last rows, which
+    stand for no tokens."""
+    lens, D, n = [5, 37], 8, 4
+    v = scan_inputs(lens, D, 1, n, F32, state=True)
+    v["A_log"][:, 0] = 100.0
+    args, kw = call_args(v)
+    out, last = kda.kda_selective_scan_fwd(*args, dev_cu(lens), **kw)
+    assert torch.isfinite(out).all() and torch.isfinite(last).all()
+    check_scan(kda, lens, v, out, last)
+
+
+def test_no_tokens(kda):
+    """Batches of empty sequences, and of none: states pass through, weights' gradients are zero."""
+    D, n = 12, 8
+    for N in (0, 3):
+        v = scan_inputs([0] * N, D, 1, n, BF)
+        args, kw = call_args(v)
+        cu = dev_cu([0] * N)
+        out, last = kda.kda_selective_scan_fwd(*args, cu, **kw)
+        assert out.shape == (0, D) and torch.equal(last, v["h0"])
+        dlast = torch.randn(N, D, n, generator=gen(1), device="cuda")
+        g = kda.kda_selective_scan_bwd(*args, cu, out, dfinal_state=dlast, **kw)
+        assert torch.equal(g["dinitial_state"], dlast)
+        assert not g["dA_log"].any() and not g["dskip"].any() and not g["ddt_bias"].any()
+        x = conv_inputs([0] * N, 1, 12, 4, BF, True, True)
+        y, window = kda.kda_short_conv_fwd(x["x"], x["w"], cu, bias=x["bias"], initial_state=x["h0"])
+        assert y.shape == (0, 1, 12) and torch.equal(window, x["h0"])
+        dw = torch.randn(x["h0"].shape, generator=gen(2), device="cuda").to(BF)
+        g = kda.kda_short_conv_bwd(x["x"], x["w"], cu, y, bias=x["bias"], initial_state=x["h0"], dfinal_state=dw)
+        assert torch.equal(g["dinitial_state"], dw) and not g["dw"].any() and not g["dbias"].any()
+    rows, w = torch.empty(0, 40, device="cuda"), torch.ones(40, device="cuda")
+    y, mean, rstd = kda.kda_layer_norm_fwd(rows, w)
+    g = kda.kda_layer_norm_bwd(rows, w, mean, rstd, rows)
+    assert y.shape == (0, 40) and not g["dw"].any() and not g["dbias"].any()
+    step = scan_inputs([], D, 1, n, BF)
+    args, kw = call_args(step)
+    assert kda.kda_selective_scan_step(*args, kw.pop("initial_state"), **kw).shape == (0, D)
+    kda.kda_sync_check()
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_scan_sequences_keep_apart(kda, bad):
     """What one sequence holds reaches no other: not its outputs, its state, nor its rows of the gradients."""
