@@ -177,6 +177,8 @@ def _stream_handle(stream, device) -> ctypes.c_void_p:
 
 
 def _need(t, name, dtype, shape, device):
+    if t is not None and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype != dtype:
@@ -783,7 +785,8 @@ def kda_selective_scan_step(u, dt, A_log, B, C, state, skip=None, z=None, dt_bia
     with _Call(u, stream) as call:
         if out is None:
             out = call.like(u)
-        _need(out, "out", u.dtype, (N, D), u.device)
+        else:
+            _need(out, "out", u.dtype, (N, D), u.device)
         st = lib.kda_selective_scan_step(_ptr(u), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(skip), _ptr(z),
                                          _ptr(dt_bias), _ptr(state), _ptr(out), code, N, D, n, G, call.handle)
     _check(st, "kda_selective_scan_step")
@@ -866,7 +869,8 @@ def kda_short_conv_step(x, w, state, bias=None, silu: bool = False, l2norm: bool
     with _Call(x, stream) as call:
         if out is None:
             out = call.like(x)
-        _need(out, "out", x.dtype, (N, H, d), x.device)
+        else:
+            _need(out, "out", x.dtype, (N, H, d), x.device)
         st = lib.kda_short_conv_step(_ptr(x), _ptr(w), _ptr(bias), _ptr(state), N, H, d, W, int(silu), int(l2norm),
                                      _ptr(out), code, call.handle)
     _check(st, "kda_short_conv_step")
