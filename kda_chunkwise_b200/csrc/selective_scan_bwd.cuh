@@ -19,7 +19,13 @@
 //                             du, ddt and the output take the places of u, delta and dy
 //   4. two sums of partial results over channel blocks (dB, dC) and over chunks (the weights)
 // Under three exponentials per (token, channel, state); sums are taken in a fixed order, so results do not
-// vary between runs.
+// vary between runs.  8192 tokens x 4096 channels x 16 states in bf16: 249 + 51 + 801 + 15 + 20 us, cold.
+// At 2048 tokens the chunk kernel has the exponential unit 62 % and the issue slots 68 % busy, the gradient kernel
+// the slots 59 % and the shared-memory data path 44 % (three blocks an SM: 168 registers, 66 KB); the chain moves
+// 268 MB.  Taken out one at a time, the sums of dB and dC over a warp's channels save 121 us of the gradient
+// kernel, the pass forwards 76, the sums over states 60, the last stage 49.  64-token chunks with eight tokens
+// recomputed at once halve the chain (35 us) but leave two blocks an SM: chunk and gradient kernel 259 + 881 us
+// against 243 + 772 in the same run.
 #pragma once
 
 #include "selective_scan.cuh"
@@ -516,29 +522,40 @@ __global__ void __launch_bounds__(kScanThreads, L > 4 ? 2 : 3) scan_bwd_grad_ker
     }
 }
 
-// dB, dC: the sum over the channel blocks of a group; W = 4 values a thread where a token's 2 n are whole fours
+// dB, dC: the sum over the channel blocks of a group; W = 4 values a thread where a token's 2 n are whole fours.
+// Eight warps of a block take every eighth channel block each.
+constexpr int kBcSlices = 8;
 template <bool BF16, int W>
-__global__ void __launch_bounds__(256) scan_bwd_bc_kernel(const ScanBwdParams p) {
+__global__ void __launch_bounds__(32 * kBcSlices) scan_bwd_bc_kernel(const ScanBwdParams p) {
+    __shared__ float s_sum[kBcSlices][32][W + 1];
     const int64_t per_token = (int64_t)p.G * 2 * p.n;
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * W;
-    if (i >= p.total_tokens * per_token) return;
-    const int64_t t = i / per_token;
-    const int x = static_cast<int>(i % per_token), g = x / (2 * p.n), w = x % (2 * p.n);
+    const int64_t i = ((int64_t)blockIdx.x * 32 + threadIdx.x) * W;
+    const bool in = i < p.total_tokens * per_token;
+    const int64_t t = in ? i / per_token : 0;
+    const int x = in ? static_cast<int>(i % per_token) : 0, g = x / (2 * p.n), w = x % (2 * p.n);
     const float *src = p.pBC + ((int64_t)g * p.cbg * p.total_tokens + t) * (2 * p.n) + w;
     const int64_t stride = p.total_tokens * 2 * p.n;
     float s[W] = {};
-#pragma unroll 16
-    for (int b = 0; b < p.cbg; ++b) {
-        if constexpr (W == 4) {
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(src + b * stride));
-            s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
-        } else {
-            s[0] += __ldg(src + b * stride);
+    if (in) {
+#pragma unroll 8
+        for (int b = threadIdx.y; b < p.cbg; b += kBcSlices) {
+            if constexpr (W == 4) {
+                const float4 v = __ldg(reinterpret_cast<const float4 *>(src + b * stride));
+                s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+            } else {
+                s[0] += __ldg(src + b * stride);
+            }
         }
     }
 #pragma unroll
-    for (int k = 0; k < W; ++k)
-        store_out(w + k < p.n ? p.dB : p.dC, (t * p.G + g) * p.n + (w + k) % p.n, !BF16, s[k]);
+    for (int k = 0; k < W; ++k) s_sum[threadIdx.y][threadIdx.x][k] = s[k];
+    __syncthreads();
+    if (threadIdx.y >= W || !in) return;
+    const int k = threadIdx.y;   // a warp a value
+    float sum = 0.f;
+#pragma unroll
+    for (int b = 0; b < kBcSlices; ++b) sum += s_sum[b][threadIdx.x][k];
+    store_out(w + k < p.n ? p.dB : p.dC, (t * p.G + g) * p.n + (w + k) % p.n, !BF16, sum);
 }
 
 // dA_log, dskip and ddt_bias: column sums over the records.  32 columns a block, kColRows rows at a time.
