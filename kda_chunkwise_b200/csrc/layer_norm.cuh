@@ -89,13 +89,16 @@ struct NormRing {
     static constexpr int kStages = !VEC ? 0 : (4 * kStage <= 131072 ? 4 : (3 * kStage <= 196608 ? 3 : 0));
     static constexpr int kBytes = kStages * kStage;
 
-    // tensor `which` of row `row` into the stage of turn `it` (zeros where there is no such row)
+    // tensor `which` of row `row` into the stage of turn `it` (zeros where there is no such row; past the row's end zeros,
+    // or with FILL its first columns again)
+    template <bool FILL = false>
     __device__ __forceinline__ static void copy(unsigned char *ring, int it, int which, const void *p, int64_t row, int d, int lane,
                                                 bool on) {
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
-            const int c = (k * RT + lane) * kE;
-            const bool in = on && c < d;
+            int c = (k * RT + lane) * kE;
+            const bool in = FILL ? on : on && c < d;
+            if (FILL && c >= d) c = 0;
             cp_async_16(smem_u32(ring) + (((it % kStages) * NT + which) * kK + k) * (NormBlock<RT>::kThreads * 16) + threadIdx.x * 16,
                         static_cast<const char *>(p) + (in ? (row * d + c) * (BF16 ? 2 : 4) : 0), in ? 16 : 0);
         }
@@ -214,8 +217,9 @@ __global__ void __launch_bounds__(NormBlock<RT>::kThreads, RT == 256 ? 2 : 1) la
     auto fetch = [&](int it) {
         if constexpr (S > 0) {
             const int64_t row = group + it * step;
-            Ring::copy(norm_ring, it, 0, p.x, row, p.d, lane, row < p.rows);
-            Ring::copy(norm_ring, it, 1, p.dy, row, p.d, lane, row < p.rows);
+            // (past the row's end the weight is zero, and xhat one of the row's own: no zero times an infinite mean rstd)
+            Ring::template copy<true>(norm_ring, it, 0, p.x, row, p.d, lane, row < p.rows);
+            Ring::template copy<true>(norm_ring, it, 1, p.dy, row, p.d, lane, row < p.rows);
             cp_async_commit();
         }
     };
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(NormBlock<RT>::kThreads, RT == 256 ? 2 : 1) la
             norm_weights<RT, E, VEC>(p.w, k, lane, p.d, wv);
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                xh[k][i] = (xh[k][i] - m) * rs;
+                xh[k][i] = (xh[k][i] - m) * (S > 0 || norm_col<RT, E, VEC>(k, i, lane) < p.d ? rs : 0.f);
                 dw[k][i] = fmaf(dy[k][i], xh[k][i], dw[k][i]);
                 db[k][i] += dy[k][i];
                 dy[k][i] *= wv[i];   // zero past d: nothing to the row's sums

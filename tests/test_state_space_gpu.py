@@ -879,3 +879,61 @@ def test_autograd_of_one_output_only(kda):
         want = kda.kda_selective_scan_bwd(v["u"], v["dt"], v["A_log"], v["B"], v["C"], cu, dout, skip=v["skip"], z=v["z"],
                                           initial_state=v["h0"], dfinal_state=torch.ones(2, D, n, device="cuda") if which else None)
         assert torch.equal(g, want["du"])
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 4), (F32, 128), (F32, 2), (BF, 512), (F32, 512)])
+def test_norm_gradients_of_large_constant_rows(kda, dtype, d):
+    """Rows of one value of 2^110 (whose mean is exact) have xhat = 0, however large mean rstd is: what lies past the
+    row's end adds nothing.  With w = 1 and dy = +-1 in turn every sum is exact and dx is rstd dy rounded once."""
+    x = torch.full((5, d), 2.0 ** 110, device="cuda", dtype=dtype)
+    w = torch.ones(d, device="cuda")
+    dy = torch.ones(5, d, device="cuda", dtype=dtype)
+    dy[:, 1::2] = -1
+    y, mean, rstd = kda.kda_layer_norm_fwd(x, w, eps=1e-12)
+    assert torch.equal(mean, torch.full_like(mean, 2.0 ** 110)) and not y.any()
+    assert float(mean[0]) * float(rstd[0]) > torch.finfo(F32).max
+    g = kda.kda_layer_norm_bwd(x, w, mean, rstd, dy)
+    assert torch.equal(g["dx"], (rstd[:, None] * dy.float()).to(dtype))
+    assert not g["dw"].any() and torch.equal(g["dbias"], dy.float().sum(0))
+
+
+def test_training_step_captured_and_replayed(kda):
+    """Forward and backward of the three operators in one graph, replayed on other inputs: the eager pass's bits."""
+    lens, D, n = [40, 0, 23], 36, 16
+    cu, T = dev_cu(lens), sum(lens)
+    p = _layer_params(D, D, n, seed=9)
+    names = ("nw", "nb", "cw", "cb", "A_log", "skip", "dt_bias")
+    data = [torch.randn(T, D, generator=gen(s), device="cuda") for s in (11, 12)]
+    B, C, dy = (torch.randn(T, *s, generator=gen(13 + i), device="cuda") for i, s in enumerate(((1, n), (1, n), (D,))))
+
+    def fresh():
+        return {k: p[k].clone().requires_grad_() for k in names}
+
+    def step(q, x):
+        for v in q.values():
+            v.grad = None
+        h = kda.layer_norm(x, q["nw"], q["nb"])
+        u, _ = kda.short_conv(h.view(T, 1, D), q["cw"], cu, bias=q["cb"], silu=True)
+        o, last = kda.selective_scan(u.view(T, D), h, q["A_log"], B, C, cu, skip=q["skip"], z=h, dt_bias=q["dt_bias"])
+        loss = (o * dy).sum() + last.sum()
+        loss.backward()
+        return [loss.detach(), *(v.grad for v in q.values())]
+
+    want = [[t.clone() for t in step(fresh(), x)] for x in data]
+    q, x = fresh(), data[0].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(q, x)
+    torch.cuda.current_stream().wait_stream(side)
+    for v in q.values():
+        v.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(q, x)
+    for i in (1, 0, 1):
+        x.copy_(data[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want[i]):
+            assert torch.equal(a, b)
