@@ -979,7 +979,11 @@ class _SelectiveScan(torch.autograd.Function):
 
 def selective_scan(u, dt, A_log, B, C, cu_seqlens, skip=None, z=None, dt_bias=None, initial_state=None):
     """kda_selective_scan_fwd as a differentiable function of every tensor but cu_seqlens; its backward is
-    kda_selective_scan_bwd.  Returns (out, final_state)."""
+    kda_selective_scan_bwd.  Returns (out, final_state).
+
+    A training step of this, short_conv and layer_norm may be captured into a CUDA graph.  As for any autograd
+    function, drop the results of earlier eager passes over the same leaves first: while one lives, the leaves'
+    gradients belong to its stream, and a capture does not allow work there."""
     return _SelectiveScan.apply(u, dt, A_log, B, C, skip, z, dt_bias, initial_state, cu_seqlens)
 
 

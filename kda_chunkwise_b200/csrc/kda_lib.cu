@@ -1243,12 +1243,15 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     return a && b && na && nb && x < y + nb && y < x + na;
 }
 
-// refuses an output that shares bytes with an input
+// refuses an output that shares bytes with an input or with another output (the workspace is one)
 struct Span { const void *p; size_t bytes; };
 kda_status apart_check(const char *where, std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
     for (const Span &o : outs)
         for (const Span &i : ins)
             if (overlap(o.p, o.bytes, i.p, i.bytes)) return fail(KDA_ERR_INVALID_ARG, std::string(where) + ": an output overlaps an input");
+    for (const Span *a = outs.begin(); a != outs.end(); ++a)
+        for (const Span *b = a + 1; b != outs.end(); ++b)
+            if (overlap(a->p, a->bytes, b->p, b->bytes)) return fail(KDA_ERR_INVALID_ARG, std::string(where) + ": an output overlaps another");
     return KDA_OK;
 }
 
@@ -1298,8 +1301,10 @@ int scan_bwd_chunk(int n) { const int L = scan_lanes(n); return L > 4 ? 64 : (L 
 
 constexpr int64_t kMaxTokens = 0x7fff0000LL;   // token counts stay 32-bit a few tiles past the end
 
+constexpr int32_t kMaxChannels = 0x1000000;    // of a token: 2 n values of each stay 32-bit
+
 bool scan_sizes_ok(int64_t rows, int32_t seqs, int32_t D, int32_t n, int32_t G) {
-    return rows >= 0 && rows <= kMaxTokens && seqs >= 0 && D > 0 && n > 0 && G > 0 && D % G == 0;
+    return rows >= 0 && rows <= kMaxTokens && seqs >= 0 && D > 0 && D <= kMaxChannels && n > 0 && G > 0 && D % G == 0;
 }
 
 // Tokens of a segment of the prompt's scan; more than total_tokens where sequences are not cut (so that
@@ -1419,11 +1424,14 @@ kda_status kda_selective_scan_fwd(const void *u, const void *dt, const float *A_
     if (initial_state != final_state && overlap(initial_state, state_bytes, final_state, state_bytes))
         return fail(KDA_ERR_INVALID_ARG, "kda_selective_scan_fwd: final_state overlaps initial_state in part");
     const size_t act = (size_t)total_tokens * D * elem_size(dtype), bc = (size_t)total_tokens * G * n * elem_size(dtype);
-    st = apart_check(where, {{out, act}, {final_state, state_bytes}}, {{u, act}, {dt, act}, {z, act}, {B, bc}, {C, bc}});
-    if (st == KDA_OK) st = apart_check(where, {{out, act}}, {{initial_state, state_bytes}, {final_state, state_bytes}});
-    if (st != KDA_OK) return st;
     const ScanSpace space = scan_space(total_tokens, num_seqs, D, n, G);
     st = space_check(where, workspace, workspace_bytes, space.total * 4);
+    if (st != KDA_OK) return st;
+    const Span out_span{out, act}, space_span{workspace, space.total * 4};
+    st = apart_check(where, {out_span, {final_state, state_bytes}, space_span},
+                     {{u, act}, {dt, act}, {z, act}, {B, bc}, {C, bc}, {A_log, (size_t)D * n * 4}, {skip, (size_t)D * 4},
+                      {dt_bias, (size_t)D * 4}, {cu_seqlens, (size_t)(num_seqs + 1LL) * 4}});
+    if (st == KDA_OK) st = apart_check(where, {out_span, space_span}, {{initial_state, state_bytes}});
     if (st != KDA_OK) return st;
     kda::ScanParams p{};
     p.u = u; p.dt = dt; p.z = z; p.B = B; p.C = C;
@@ -1471,8 +1479,8 @@ kda_status kda_selective_scan_step(const void *u, const void *dt, const float *A
     if (st != KDA_OK) return st;
     const size_t act = (size_t)N * D * elem_size(dtype), bc = (size_t)N * G * n * elem_size(dtype);
     const Span st_span{state, (size_t)N * D * n * 4};
-    st = apart_check(where, {{out, act}, st_span}, {{u, act}, {dt, act}, {z, act}, {B, bc}, {C, bc}});
-    if (st == KDA_OK) st = apart_check(where, {{out, act}}, {st_span});
+    st = apart_check(where, {{out, act}, st_span}, {{u, act}, {dt, act}, {z, act}, {B, bc}, {C, bc}, {A_log, (size_t)D * n * 4},
+                                                    {skip, (size_t)D * 4}, {dt_bias, (size_t)D * 4}});
     if (st != KDA_OK) return st;
     kda::ScanStepParams p{};
     p.u = u; p.dt = dt; p.z = z; p.B = B; p.C = C;
@@ -1548,11 +1556,15 @@ kda_status kda_selective_scan_bwd(const void *u, const void *dt, const float *A_
                        {A_log, skip, dt_bias, cu_seqlens, initial_state, dfinal_state, dinitial_state, dA_log, dskip, ddt_bias}, workspace);
     if (st != KDA_OK) return st;
     const size_t act = (size_t)total_tokens * D * elem_size(dtype), bc = (size_t)total_tokens * G * n * elem_size(dtype);
-    st = apart_check(where, {{du, act}, {ddt, act}, {dz, act}, {dB, bc}, {dC, bc}},
-                     {{u, act}, {dt, act}, {z, act}, {dout, act}, {B, bc}, {C, bc}});
-    if (st != KDA_OK) return st;
     const ScanBwdSpace space = scan_bwd_space(total_tokens, num_seqs, D, n, G);
     st = space_check(where, workspace, workspace_bytes, space.total * 4);
+    if (st != KDA_OK) return st;
+    const size_t state_bytes = (size_t)num_seqs * D * n * 4, A_bytes = (size_t)D * n * 4, per_channel = (size_t)D * 4;
+    st = apart_check(where, {{du, act}, {ddt, act}, {dz, act}, {dB, bc}, {dC, bc}, {dA_log, A_bytes}, {dskip, per_channel},
+                             {ddt_bias, per_channel}, {dinitial_state, state_bytes}, {workspace, space.total * 4}},
+                     {{u, act}, {dt, act}, {z, act}, {dout, act}, {B, bc}, {C, bc}, {A_log, A_bytes}, {skip, per_channel},
+                      {dt_bias, per_channel}, {initial_state, state_bytes}, {dfinal_state, state_bytes},
+                      {cu_seqlens, (size_t)(num_seqs + 1LL) * 4}});
     if (st != KDA_OK) return st;
     kda::ScanBwdParams p{};
     p.u = u; p.dt = dt; p.z = z; p.B = B; p.C = C; p.dout = dout;
@@ -1629,7 +1641,7 @@ int64_t conv_bwd_runs(int64_t T, int64_t C) {
 }
 
 bool conv_sizes_ok(int64_t rows, int32_t seqs, int32_t H, int32_t d) {
-    return rows >= 0 && rows <= kMaxTokens && seqs >= 0 && H > 0 && d > 0 && (int64_t)H * d <= 0x1000000LL;
+    return rows >= 0 && rows <= kMaxTokens && seqs >= 0 && H > 0 && d > 0 && (int64_t)H * d <= kMaxChannels;
 }
 
 kda_status conv_check(const char *where, int64_t rows, int32_t seqs, int32_t H, int32_t d, int32_t width, int32_t l2norm,
@@ -1671,8 +1683,9 @@ kda_status kda_short_conv_fwd(const void *x, const float *w, const float *bias, 
     const int64_t C = (int64_t)H * d;
     const size_t es = elem_size(dtype), rows_bytes = (size_t)total_tokens * C * es;
     const size_t state_bytes = (size_t)num_seqs * (width - 1) * C * es;
-    st = apart_check(where, {{y, rows_bytes}, {final_state, state_bytes}}, {{x, rows_bytes}});
-    if (st == KDA_OK) st = apart_check(where, {{y, rows_bytes}}, {{initial_state, state_bytes}, {final_state, state_bytes}});
+    st = apart_check(where, {{y, rows_bytes}, {final_state, state_bytes}},
+                     {{x, rows_bytes}, {w, (size_t)C * width * 4}, {bias, (size_t)C * 4}, {cu_seqlens, (size_t)(num_seqs + 1LL) * 4}});
+    if (st == KDA_OK) st = apart_check(where, {{y, rows_bytes}}, {{initial_state, state_bytes}});
     if (st != KDA_OK) return st;
     if (initial_state != final_state && overlap(initial_state, state_bytes, final_state, state_bytes))
         return fail(KDA_ERR_INVALID_ARG, "kda_short_conv_fwd: final_state overlaps initial_state in part");
@@ -1728,8 +1741,7 @@ kda_status kda_short_conv_step(const void *x, const float *w, const float *bias,
     const int64_t C = (int64_t)H * d;
     const size_t rows_bytes = (size_t)N * C * elem_size(dtype);
     const Span st_span{state, rows_bytes * (width - 1)};
-    st = apart_check(where, {{y, rows_bytes}, st_span}, {{x, rows_bytes}});
-    if (st == KDA_OK) st = apart_check(where, {{y, rows_bytes}}, {st_span});
+    st = apart_check(where, {{y, rows_bytes}, st_span}, {{x, rows_bytes}, {w, (size_t)C * width * 4}, {bias, (size_t)C * 4}});
     if (st != KDA_OK) return st;
     kda::ConvStateParams p{};
     p.x = x; p.w = w; p.bias = bias;
@@ -1787,9 +1799,13 @@ kda_status kda_short_conv_bwd(const void *x, const float *w, const float *bias, 
                        workspace);
     if (st != KDA_OK) return st;
     const size_t rows_bytes = (size_t)total_tokens * C * elem_size(dtype);
-    st = apart_check(where, {{dx, rows_bytes}}, {{x, rows_bytes}, {dy, rows_bytes}});
+    const size_t space = kda_short_conv_bwd_workspace_size(total_tokens, H, d, width);
+    st = space_check(where, workspace, workspace_bytes, space);
     if (st != KDA_OK) return st;
-    st = space_check(where, workspace, workspace_bytes, kda_short_conv_bwd_workspace_size(total_tokens, H, d, width));
+    const size_t state_bytes = (size_t)num_seqs * (width - 1) * C * elem_size(dtype), w_bytes = (size_t)C * width * 4;
+    st = apart_check(where, {{dx, rows_bytes}, {dw, w_bytes}, {dbias, (size_t)C * 4}, {dinitial_state, state_bytes}, {workspace, space}},
+                     {{x, rows_bytes}, {dy, rows_bytes}, {w, w_bytes}, {bias, (size_t)C * 4}, {initial_state, state_bytes},
+                      {dfinal_state, state_bytes}, {cu_seqlens, (size_t)(num_seqs + 1LL) * 4}});
     if (st != KDA_OK) return st;
     kda::ConvStateParams p{};
     p.x = x; p.dy = dy; p.w = w; p.bias = bias; p.cu = cu_seqlens;
@@ -1868,7 +1884,8 @@ kda_status kda_layer_norm_fwd(const void *x, const float *w, const float *b, int
     st = aligned_check(where, elem_size(dtype), {x, y}, {w, b, mean, rstd});
     if (st != KDA_OK) return st;
     const size_t bytes = (size_t)rows * d * elem_size(dtype);
-    st = apart_check(where, {{y, bytes}}, {{x, bytes}});
+    st = apart_check(where, {{y, bytes}, {mean, (size_t)rows * 4}, {rstd, (size_t)rows * 4}},
+                     {{x, bytes}, {w, (size_t)d * 4}, {b, (size_t)d * 4}});
     if (st != KDA_OK) return st;
     kda::NormParams p{};
     p.x = x; p.w = w; p.b = b;
@@ -1913,9 +1930,11 @@ kda_status kda_layer_norm_bwd(const void *x, const float *w, const float *mean, 
     st = aligned_check(where, elem_size(dtype), {x, dy, dx}, {w, mean, rstd, dw, db}, workspace);
     if (st != KDA_OK) return st;
     const size_t bytes = (size_t)rows * d * elem_size(dtype);
-    st = apart_check(where, {{dx, bytes}}, {{x, bytes}, {dy, bytes}});
+    const size_t space = kda_layer_norm_bwd_workspace_size(rows, d);
+    st = space_check(where, workspace, workspace_bytes, space);
     if (st != KDA_OK) return st;
-    st = space_check(where, workspace, workspace_bytes, kda_layer_norm_bwd_workspace_size(rows, d));
+    st = apart_check(where, {{dx, bytes}, {dw, (size_t)d * 4}, {db, (size_t)d * 4}, {workspace, space}},
+                     {{x, bytes}, {dy, bytes}, {w, (size_t)d * 4}, {mean, (size_t)rows * 4}, {rstd, (size_t)rows * 4}});
     if (st != KDA_OK) return st;
     kda::NormParams p{};
     p.x = x; p.dy = dy; p.w = w;

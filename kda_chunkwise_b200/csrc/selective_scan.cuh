@@ -11,8 +11,9 @@
 // channel) (softplus, the gate) is done once, not once per state.
 //   - A channel's n states lie on L = 2^ceil(log2(n / 4)) lanes, four to a lane; 128 threads scan
 //     KC x 128 / L channels of one group over one segment of one sequence.
-//   - 256 more threads (128 where two blocks share an SM) stage the next tile of tokens and write the outputs of the last one meanwhile, so
-//     that the scanning warps only scan: with one sequence there is about one of them per scheduler.
+//   - 256 more threads (128 where two blocks share an SM) stage the next tile of tokens and write the
+//     outputs of the last one meanwhile, so that the scanning warps only scan: with one sequence there is
+//     about one of them per scheduler.
 //   - What a scanning thread reads from shared memory per token is the next bound: B and C lie next to
 //     each other, in bf16 where they came in bf16, and serve the KC channels of a thread.
 //   - The sum over the states is taken for L tokens at once (transposed_sums): one value a lane.

@@ -253,3 +253,34 @@ def test_binding_refuses_what_the_kernels_do_not_take():
         kda.kda_layer_norm_fwd(f(4, 8, dtype=torch.float16), f(8))
     with pytest.raises(ValueError):
         kda.kda_layer_norm_fwd(f(4, 8), f(7))
+
+
+OVERLAPS = [   # outputs over weights, carried states, each other and the workspace
+    (scan_fwd, dict(out=_p(2))), (scan_fwd, dict(hN=_p(2))), (scan_fwd, dict(skip=_p(9), out=_p(9))), (scan_fwd, dict(hN=_p(5))),
+    (scan_step, dict(state=_p(2))), (scan_step, dict(out=_p(2))),
+    (scan_bwd, dict(h0=_p(13), dh0=_p(13))), (scan_bwd, dict(dhN=_p(13), dh0=_p(13))), (scan_bwd, dict(ddt=_p(7))),
+    (scan_bwd, dict(dA_log=_p(2))), (scan_bwd, dict(dC=_p(10))), (scan_bwd, dict(ws=_p(0))), (scan_bwd, dict(ws=_p(7))),
+    (scan_bwd, dict(dskip=_p(9))), (scan_bwd, dict(dt_bias=_p(13), ddt_bias=_p(13))), (scan_bwd, dict(dh0=_p(6))),
+    (conv_fwd, dict(y=_p(1))), (conv_fwd, dict(hN=_p(1))), (conv_step, dict(state=_p(1))),
+    (conv_bwd, dict(h0=_p(8), dh0=_p(8))), (conv_bwd, dict(dhN=_p(8), dh0=_p(8))), (conv_bwd, dict(dh0=_p(4))),
+    (conv_bwd, dict(dw=_p(1))), (conv_bwd, dict(dbias=_p(5))), (conv_bwd, dict(ws=_p(3))), (conv_bwd, dict(ws=_p(4))),
+    (norm_fwd, dict(y=_p(1))), (norm_fwd, dict(mean=_p(4))), (norm_fwd, dict(rstd=_p(2))),
+    (norm_bwd, dict(dw=_p(1))), (norm_bwd, dict(db=_p(6))), (norm_bwd, dict(dx=_p(2))), (norm_bwd, dict(ws=_p(0))),
+    (norm_bwd, dict(ws=_p(5))),
+]
+
+
+@pytest.mark.parametrize("call,kw", OVERLAPS, ids=[f"{c.__name__}-{i}" for i, (c, _) in enumerate(OVERLAPS)])
+def test_overlaps_are_refused(call, kw):
+    before = kda.kda_launch_count()
+    assert call(**kw) == INVALID
+    assert b"overlaps" in lib.kda_last_error()
+    assert kda.kda_launch_count() == before
+
+
+@pytest.mark.parametrize("call", [scan_fwd, scan_step, scan_bwd])
+def test_more_channels_than_the_kernels_count_are_refused(call):
+    before = kda.kda_launch_count()
+    assert call(D=(1 << 24) + 1, n=1) == INVALID
+    assert kda.kda_launch_count() == before
+    assert kda.kda_selective_scan_bwd_workspace_size(8, 1, (1 << 24) + 1, 1) == 0
