@@ -7,9 +7,8 @@
 //
 // All three are bound by memory (about 10 flops a byte at most): each input is read once, its
 // neighbours in time come from registers, and a thread keeps several rows in flight, in a ring in shared
-// memory that it alone reads.  A thread owns E channels: consecutive ones, moved as one vector, where the
-// rows allow it, else channels a block apart, so that single elements are still read side by side (and
-// then a batch of rows in registers).  8192 x 4096 channels, W = 4, SiLU and unit rows, bf16: forward
+// memory that it alone reads.  A thread owns E channels, laid out as ConvCols says; where they are not moved as
+// vectors, a batch of rows is in registers instead.  8192 x 4096 channels, W = 4, SiLU and unit rows, bf16: forward
 // 38 us (134 MB, 3.6 TB/s), backward 75 us + 6 for the weights' sums (201 MB, 2.7 TB/s).  Both are held by
 // instructions more than by memory: 44 % and 53 % of the issue slots busy at four blocks an SM.
 #pragma once
@@ -37,15 +36,24 @@ struct ConvStateParams {
     bool silu, l2norm;
 };
 
-// The channels of a thread: c0 + i step (VEC: consecutive, moved as vectors).
-template <bool BF16, int E, bool VEC>
+// How a thread's E channels lie.
+enum class ConvCols {
+    kVector,     // consecutive, moved as one vector: where the rows allow it
+    kApart,      // a block's threads apart, moved one by one: single elements are still read side by side
+    kTogether,   // consecutive, moved one by one: with l2norm, since a head's sum is taken over a thread's channels and
+                 // its neighbours'
+};
+
+// The channels of a thread: c0 + i step.
+template <bool BF16, int E, ConvCols COLS>
 struct ChannelGroup {
+    static constexpr bool VEC = COLS == ConvCols::kVector;
+    static constexpr int step = COLS == ConvCols::kApart ? kConvThreads : 1;
     int64_t c0;
-    static constexpr int step = VEC ? 1 : kConvThreads;
     int count;   // how many of the E are channels
 
     __device__ __forceinline__ ChannelGroup(int64_t block, int C) {
-        c0 = block * kConvThreads * E + (VEC ? (int64_t)threadIdx.x * E : threadIdx.x);
+        c0 = block * kConvThreads * E + (step == 1 ? (int64_t)threadIdx.x * E : threadIdx.x);
         const int64_t n = c0 < C ? (C - c0 + step - 1) / step : 0;
         count = static_cast<int>(n > E ? E : n);
     }
@@ -212,9 +220,10 @@ constexpr int kConvUnroll = 6;   // rows of one turn of a loop: a multiple of ev
 
 // Rows on their way: a ring whose slot i % kConvRows holds row i of a run, or (not VEC) the rows of one turn in
 // registers.
-template <bool BF16, int E, bool VEC>
+template <bool BF16, int E, ConvCols COLS>
 struct ConvRows {
-    using Group = ChannelGroup<BF16, E, VEC>;
+    using Group = ChannelGroup<BF16, E, COLS>;
+    static constexpr bool VEC = Group::VEC;
     static constexpr int kSlot = kConvThreads * Group::kVec;
     static constexpr int kBytes = VEC ? kConvRows * kSlot : 16;
     unsigned char *ring;
@@ -234,12 +243,12 @@ struct ConvRows {
 
 // grid: x = runs of run_len tokens, then one block per sequence for the final states; y = blocks of
 // channels.  With hN = h0 the two are separate launches (first_block skips the runs).
-template <bool BF16, int W, int E, bool VEC>
+template <bool BF16, int W, int E, ConvCols COLS>
 __global__ void __launch_bounds__(kConvThreads) conv_state_fwd_kernel(const ConvStateParams p) {
     constexpr int N = E / 2;
-    using Rows = ConvRows<BF16, E, VEC>;
+    using Rows = ConvRows<BF16, E, COLS>;
     __shared__ __align__(16) unsigned char slots[Rows::kBytes];
-    const ChannelGroup<BF16, E, VEC> cg(blockIdx.y, p.C);
+    const ChannelGroup<BF16, E, COLS> cg(blockIdx.y, p.C);
     Rows xs;
     xs.ring = slots;
     xs.p = p.x;
@@ -304,10 +313,10 @@ __global__ void __launch_bounds__(kConvThreads) conv_state_fwd_kernel(const Conv
 }
 
 // One token of num_seqs sequences; the state (hN) in place.  A block walks over rows of the batch.
-template <bool BF16, int W, int E, bool VEC>
+template <bool BF16, int W, int E, ConvCols COLS>
 __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(const ConvStateParams p) {
     constexpr int N = E / 2;
-    const ChannelGroup<BF16, E, VEC> cg(blockIdx.y, p.C);
+    const ChannelGroup<BF16, E, COLS> cg(blockIdx.y, p.C);
     const int lanes = p.d / E;
     f32x2 w[W][N], bias[N];
     load_taps<W, E>(p, cg, w, bias);
@@ -329,12 +338,12 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(const ConvState
 //   dx_u = sum_{i < W} w[W-1-i] q_{u+i}    (tokens of the same sequence only).
 // A run reads W - 1 tokens past its end to complete its last inputs.  Positions before a sequence's
 // first token are the rows of its carried state.
-template <bool BF16, int W, int E, bool VEC>
+template <bool BF16, int W, int E, ConvCols COLS>
 __global__ void __launch_bounds__(kConvThreads) conv_state_bwd_kernel(const ConvStateParams p) {
     constexpr int N = E / 2;
-    using Rows = ConvRows<BF16, E, VEC>;
+    using Rows = ConvRows<BF16, E, COLS>;
     __shared__ __align__(16) unsigned char slots[2 * Rows::kBytes];
-    const ChannelGroup<BF16, E, VEC> cg(blockIdx.y, p.C);
+    const ChannelGroup<BF16, E, COLS> cg(blockIdx.y, p.C);
     Rows xs, ds;   // of x, of dy
     xs.ring = slots;
     ds.ring = slots + Rows::kBytes;

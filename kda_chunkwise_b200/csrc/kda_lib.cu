@@ -1665,6 +1665,15 @@ kda_status with_width(int width, F f) {
     }
 }
 
+// f(integral_constant<ConvCols, how a thread's channels lie>)
+template <class F>
+kda_status with_cols(bool vec, bool l2norm, F f) {
+    using kda::ConvCols;
+    if (vec) return f(std::integral_constant<ConvCols, ConvCols::kVector>());
+    if (l2norm) return f(std::integral_constant<ConvCols, ConvCols::kTogether>());
+    return f(std::integral_constant<ConvCols, ConvCols::kApart>());
+}
+
 }  // namespace
 
 kda_status kda_short_conv_fwd(const void *x, const float *w, const float *bias, const int32_t *cu_seqlens, int32_t num_seqs,
@@ -1716,12 +1725,12 @@ kda_status kda_short_conv_fwd(const void *x, const float *w, const float *bias, 
             const bool apart = states > 0 && final_state == initial_state && p.runs > 0;
             const int64_t first = apart ? p.runs : p.runs + states;
             if (first == 0) return KDA_OK;
-            return with_flag(vec, [&](auto v) {
-                constexpr bool VEC = decltype(v)::value;
-                kda::conv_state_fwd_kernel<kBf16, W, E, VEC><<<dim3((unsigned)first, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
+            return with_cols(vec, p.l2norm, [&](auto c) {
+                constexpr kda::ConvCols kCols = decltype(c)::value;
+                kda::conv_state_fwd_kernel<kBf16, W, E, kCols><<<dim3((unsigned)first, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
                 if (apart) {
                     p.first_block = p.runs;
-                    kda::conv_state_fwd_kernel<kBf16, W, E, VEC><<<dim3((unsigned)states, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
+                    kda::conv_state_fwd_kernel<kBf16, W, E, kCols><<<dim3((unsigned)states, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
                 }
                 return launched("short_conv_fwd launch", apart ? 2 : 1);
             });
@@ -1760,10 +1769,10 @@ kda_status kda_short_conv_step(const void *x, const float *w, const float *bias,
             constexpr int W = decltype(taps)::value, E = kConvBwdElems;
             const int64_t cblocks = conv_channel_blocks(C, E);
             if (cblocks > 65535) return fail(KDA_ERR_INVALID_ARG, "kda_short_conv_step: too many channels");
-            return with_flag(C % E == 0 && all_aligned({x, y, state}), [&](auto v) {
+            return with_cols(C % E == 0 && all_aligned({x, y, state}), p.l2norm, [&](auto c) {
                 // as many blocks as run at once, each walking over rows of the batch (the taps are read once)
                 const int64_t rows = std::min<int64_t>(N, std::max<int64_t>(1, 7LL * device_sm_count() / cblocks));
-                kda::conv_step_kernel<kBf16, W, E, decltype(v)::value>
+                kda::conv_step_kernel<kBf16, W, E, decltype(c)::value>
                     <<<dim3((unsigned)rows, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
                 return launched("short_conv_step launch");
             });
@@ -1829,8 +1838,8 @@ kda_status kda_short_conv_bwd(const void *x, const float *w, const float *bias, 
         return with_width(width, [&](auto taps) {
             constexpr bool kBf16 = decltype(bf16)::value;
             constexpr int W = decltype(taps)::value;
-            return with_flag(vec, [&](auto v) {
-                kda::conv_state_bwd_kernel<kBf16, W, kConvBwdElems, decltype(v)::value>
+            return with_cols(vec, p.l2norm, [&](auto c) {
+                kda::conv_state_bwd_kernel<kBf16, W, kConvBwdElems, decltype(c)::value>
                     <<<dim3((unsigned)p.runs, (unsigned)cblocks), kda::kConvThreads, 0, s>>>(p);
                 const int64_t cols = (W + 1) * C;
                 kda::conv_weight_sum_kernel<<<(unsigned)((cols + 31) / 32), dim3(32, kda::kSumRows), 0, s>>>(p.part, p.runs, p.C, W, dw, dbias);

@@ -937,3 +937,45 @@ def test_training_step_captured_and_replayed(kda):
         torch.cuda.synchronize()
         for a, b in zip(got, want[i]):
             assert torch.equal(a, b)
+
+
+# ---- convolution with unit rows on tensors off the vector grid -------------------------------------
+
+
+def off_grid(x):
+    """The same values one element past the 16-byte grid."""
+    return torch.cat([x.flatten()[:1], x.flatten()])[1:].view(x.shape) if x.numel() else x
+
+
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("H,d", [(1, 64), (3, 64), (1, 128), (3, 128), (20, 64)])
+@pytest.mark.parametrize("W", [1, 3, 4])
+def test_conv_unit_rows_off_the_vector_grid(kda, H, d, W, t):
+    """One tensor at a time (the carried state alone among them), then all: prompts, single tokens and gradients."""
+    lens, silu, bias = [70, 0, 130, 5], W != 3, W != 1
+    v = conv_inputs(lens, H, d, W, t, bias, True, seed=W)
+    dy = torch.randn(v["x"].shape, generator=gen(9), device="cuda").to(t)
+    dlast = torch.randn(v["h0"].shape, generator=gen(10), device="cuda").to(t)
+    ry, rlast, ys, rg, scale = conv_refs(lens, v, silu, True, dy, dlast)
+    one = conv_inputs([1] * 5, H, d, W, t, bias, True, seed=W + 1)
+    oy, olast, oys = conv_refs([1] * 5, one, silu, True)
+    cu = dev_cu(lens)
+    for moved in (("x",), ("out",), ("initial_state",), ("final_state",), ("dy",), ("dfinal_state",),
+                  ("x", "out", "initial_state", "final_state", "dy", "dfinal_state")):
+        at = lambda name, x: off_grid(x) if name in moved else x  # noqa: E731
+        y, last = kda.kda_short_conv_fwd(at("x", v["x"]), v["w"], cu, bias=v["bias"], initial_state=at("initial_state", v["h0"]),
+                                         silu=silu, l2norm=True, out=at("out", torch.zeros_like(v["x"])),
+                                         final_state=at("final_state", torch.zeros_like(v["h0"])))
+        check(f"{moved} y", y, ry, ys, 2.0 ** -20)
+        assert np.array_equal(host(last), rlast), moved
+        state = at("initial_state", one["h0"].clone())
+        y = kda.kda_short_conv_step(at("x", one["x"]), one["w"], state, bias=one["bias"], silu=silu, l2norm=True,
+                                    out=at("out", torch.zeros_like(one["x"])))
+        check(f"{moved} step", y, oy, oys, 2.0 ** -20)
+        assert np.array_equal(host(state), olast), moved
+        g = kda.kda_short_conv_bwd(at("x", v["x"]), v["w"], cu, at("dy", dy), bias=v["bias"],
+                                   initial_state=at("initial_state", v["h0"]), dfinal_state=at("dfinal_state", dlast), silu=silu,
+                                   l2norm=True)
+        for k in ("dx", "dw", "dinitial_state") + (("dbias",) if bias else ()):
+            check(f"{moved} {k}", g[k], rg[k], scale[k], 2.0 ** -19 + (sum(lens) * 2.0 ** -24 if k in ("dw", "dbias") else 0.0))
+    kda.kda_sync_check()
