@@ -28,6 +28,9 @@
 // against 243 + 772 in the same run.
 #pragma once
 
+#include <cfloat>
+#include <type_traits>
+
 #include "selective_scan.cuh"
 
 namespace kda {
@@ -360,8 +363,9 @@ __global__ void __launch_bounds__(kScanThreads, L > 4 ? 2 : 3) scan_bwd_grad_ker
     // backwards
     const int tokens = static_cast<int>(at.t1 - at.t0);
     float *bc_out = p.pBC + ((int64_t)cb * p.total_tokens + at.t0) * (2 * p.n);
-#pragma unroll 1
-    for (int sb = blocks - 1; sb >= 0; --sb) {
+    // kBack tokens; PAD: rows that stand for no token among them
+    auto block = [&](int sb, auto pad) {
+        constexpr bool PAD = decltype(pad)::value;
         const int tb = sb * kBack;
         f32x2 a01[kBack][KC], a23[kBack][KC], p01[kBack][KC], p23[kBack][KC];   // a_t and a_t h_{t-1}
 #pragma unroll
@@ -405,7 +409,9 @@ __global__ void __launch_bounds__(kScanThreads, L > 4 ? 2 : 3) scan_bwd_grad_ker
                 const f32x2 hh01 = f2_fma(du, b01, p01[i][k]), hh23 = f2_fma(du, b23, p23[i][k]);
                 g01[k] = f2_fma(c01, dy, g01[k]);
                 g23[k] = f2_fma(c23, dy, g23[k]);
-                const f32x2 e01 = f2_mul(g01[k], p01[i][k]), e23 = f2_mul(g23[k], p23[i][k]);
+                f32x2 e01 = f2_mul(g01[k], p01[i][k]), e23 = f2_mul(g23[k], p23[i][k]);
+                // (no token: a = 1 and g comes from after the chunk, so that e would be large, or infinite, and no term)
+                if (PAD && tb + i >= tokens) e01 = e23 = 0ull;
                 dA01[k] = f2_fma(e01, dd, dA01[k]);
                 dA23[k] = f2_fma(e23, dd, dA23[k]);
                 float lo, hi;
@@ -475,7 +481,11 @@ __global__ void __launch_bounds__(kScanThreads, L > 4 ? 2 : 3) scan_bwd_grad_ker
                 bc_out[t * (2 * p.n) + (x / (4 * L)) * p.n + m] = s;
             }
         }
-    }
+    };
+    int sb = blocks - 1;
+    if (tokens % kBack != 0) block(sb--, std::true_type());   // (code of its own: tested in the loop it costs 1 % and more)
+#pragma unroll 1
+    for (; sb >= 0; --sb) block(sb, std::false_type());
 #pragma unroll 2
     for (int i = 0; i < Tile::kR && i * (kScanThreads / Tile::kFR) < tokens; ++i) {
         const int on = at.on(i), x = at.row(i) * YS + at.col();
@@ -579,9 +589,14 @@ __global__ void __launch_bounds__(32 * kColRows) scan_bwd_weights_kernel(const S
     if (threadIdx.y != 0 || col >= nA + 2 * p.D) return;
 #pragma unroll
     for (int k = 1; k < kColRows; ++k) s += s_sum[k][threadIdx.x];
-    if (col < nA) p.dA_log[col] = -expf(p.A_log[col]) * s;
-    else if (col < nA + p.D) { if (p.dskip) p.dskip[col - nA] = s; }
-    else if (p.ddt_bias) p.ddt_bias[col - nA - p.D] = s;
+    if (col < nA) {
+        const float A = -expf(p.A_log[col]);
+        p.dA_log[col] = (A < -FLT_MAX ? -FLT_MAX : A) * s;   // finite (as load_decay): a sum of zero stays zero; a NaN stays one
+    } else if (col < nA + p.D) {
+        if (p.dskip) p.dskip[col - nA] = s;
+    } else if (p.ddt_bias) {
+        p.ddt_bias[col - nA - p.D] = s;
+    }
 }
 
 }  // namespace kda

@@ -979,3 +979,39 @@ def test_conv_unit_rows_off_the_vector_grid(kda, H, d, W, t):
         for k in ("dx", "dw", "dinitial_state") + (("dbias",) if bias else ()):
             check(f"{moved} {k}", g[k], rg[k], scale[k], 2.0 ** -19 + (sum(lens) * 2.0 ** -24 if k in ("dw", "dbias") else 0.0))
     kda.kda_sync_check()
+
+
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D,n", [(8, 4), (40, 8), (40, 16), (20, 32), (9, 64)])
+def test_scan_backward_past_the_largest_float(kda, D, n, t):
+    """Decays past the largest fp32 value backwards: a state that is forgotten at once has no gradient, and neither
+    that of A_log nor the rows that fill up a chunk's last tokens (whose decay is one) turn it into NaN."""
+    lens = [5, 37, 0, 64, 3]
+    v = scan_inputs(lens, D, 1, n, t, state=True)
+    v["A_log"][:, 0] = 100.0
+    v["A_log"][:3] = 88.8
+    args, kw = call_args(v)
+    dout = torch.randn(sum(lens), D, generator=gen(3), device="cuda").to(t)
+    dlast = 4 * torch.randn(len(lens), D, n, generator=gen(4), device="cuda")
+    g = kda.kda_selective_scan_bwd(*args, dev_cu(lens), dout, dfinal_state=dlast, **kw)
+    for k, x in g.items():
+        assert torch.isfinite(x).all(), k
+    assert not g["dA_log"][:, 0].any() and not g["dA_log"][:3].any()
+    check_scan_grads(lens, v, dout, dlast, g)
+
+
+@pytest.mark.parametrize("n", [4, 11, 16, 64])
+@pytest.mark.parametrize("T", [5, 33, 70])
+def test_scan_backward_infinite_last_input(kda, T, n):
+    """The gradient of A_log and of the initial state does not depend on the last token's input, also where that is
+    infinite and rows that stand for no token follow it."""
+    v = scan_inputs([T], 12, 1, n, F32)
+    dout = torch.randn(T, 12, generator=gen(3), device="cuda")
+    dlast = torch.randn(1, 12, n, generator=gen(4), device="cuda")
+    got = []
+    for last in (1.0, float("inf")):
+        v["u"][-1] = last
+        args, kw = call_args(v)
+        got.append(kda.kda_selective_scan_bwd(*args, dev_cu([T]), dout, dfinal_state=dlast, **kw))
+    for k in ("dA_log", "dinitial_state"):
+        assert torch.isfinite(got[0][k]).all() and torch.equal(got[0][k], got[1][k]), k
