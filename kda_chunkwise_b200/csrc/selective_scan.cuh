@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kScanStepThreads) scan_step_kernel(const ScanS
             store_piece<false, 4, false>(p.state, x * p.n + m0, v4, h);
         }
         if (lane == 0 && active) {
-            y = fmaf(skip, u[0], y);
+            if (p.skip) y = fmaf(skip, u[0], y);   // (no skip is no term: zero times an infinite u would be one)
             if (p.z) y *= silu(z[0]);
             store_out(p.out, x, !BF16, y);
         }

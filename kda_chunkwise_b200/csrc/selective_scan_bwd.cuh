@@ -454,9 +454,10 @@ __global__ void __launch_bounds__(kScanThreads, L > 4 ? 2 : 3) scan_bwd_grad_ker
                 const int x = t * YS + chl + k * Tile::kStep;
                 const float d = s_delta[x], u = s_u[x], dy = s_dy[x];
                 const float ddt = fmaf(u, dbu, 0.6931471805599453f * ddA) * one_minus_exp_neg(d);   // sigmoid(x) = 1 - exp(-softplus(x))
-                s_u[x] = fmaf(d, dbu, skip[k] * dy);
+                // (no skip is no term: zero times an infinite u or dy would be one)
+                s_u[x] = fmaf(d, dbu, p.skip ? skip[k] * dy : 0.f);
                 s_delta[x] = ddt;
-                s_dy[x] = fmaf(skip[k], u, y);
+                s_dy[x] = p.skip ? fmaf(skip[k], u, y) : y;
                 dskip[k] = fmaf(dy, u, dskip[k]);
                 dbias[k] += ddt;
             };

@@ -1015,3 +1015,26 @@ def test_scan_backward_infinite_last_input(kda, T, n):
         got.append(kda.kda_selective_scan_bwd(*args, dev_cu([T]), dout, dfinal_state=dlast, **kw))
     for k in ("dA_log", "dinitial_state"):
         assert torch.isfinite(got[0][k]).all() and torch.equal(got[0][k], got[1][k]), k
+
+
+def test_scan_without_skip_keeps_infinities(kda):
+    """No skip means no term: an infinite input or gradient is not multiplied by zero.  All terms are positive, so the
+    formulas give plus infinity from the infinite token on (outputs, states) or up to it (gradients)."""
+    T, D, n, at, up = 6, 8, 4, 3, float("inf")
+    one = lambda *s: torch.ones(s, device="cuda")  # noqa: E731
+    u, dt, A_log, BC = one(T, D), one(T, D), torch.zeros(D, n, device="cuda"), one(T, 1, n)
+    u[at] = up
+    out, last = kda.kda_selective_scan_fwd(u, dt, A_log, BC, BC, dev_cu([T]))
+    assert torch.isfinite(out[:at]).all() and (out[at:] == up).all() and (last == up).all()
+    state, rows = torch.zeros(1, D, n, device="cuda"), []
+    for i in range(T):
+        rows.append(kda.kda_selective_scan_step(u[i:i + 1], dt[i:i + 1], A_log, BC[i:i + 1], BC[i:i + 1], state))
+    rows = torch.cat(rows)
+    assert torch.isfinite(rows[:at]).all() and (rows[at:] == up).all() and (state == up).all()
+    dout = one(T, D)
+    dout[at] = up
+    g = kda.kda_selective_scan_bwd(one(T, D), dt, A_log, BC, BC, dev_cu([T]), dout)
+    assert (g["du"][:at + 1] == up).all() and torch.isfinite(g["du"][at + 1:]).all()
+    # the output enters the gate's gradient: dz = dout y silu'(z)
+    g = kda.kda_selective_scan_bwd(u, dt, A_log, BC, BC, dev_cu([T]), one(T, D), z=one(T, D))
+    assert torch.isfinite(g["dz"][:at]).all() and (g["dz"][at:] == up).all()
