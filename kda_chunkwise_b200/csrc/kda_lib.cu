@@ -1350,17 +1350,26 @@ kda_status launch_scan_pass(const kda::ScanParams &p, int64_t blocks, cudaStream
     return launched("selective_scan_fwd launch");
 }
 
-// Two blocks an SM with half the staging threads where there are blocks for it (36 ragged short sequences 294 us
-// against 677 with one block an SM; 16384 channels of one long sequence 1147 against 1188); one block with all of
-// the staging threads otherwise.
+// Two blocks an SM with half the staging threads where there are blocks for it and both fit, which is so in bf16 (36
+// ragged short sequences of 4091 channels and 64 states 297 us against 487 with one block an SM; 16384 channels of one
+// sequence 1097 against 1165; 9 prompts of 2048 channels 107 against 102).  In fp32 only one fits, and it wants all of
+// the staging threads (8192 tokens of 4096 channels in four sequences, 16 states: 309 us against 368 with half of them; 8
+// states, ten sequences: 207 against 297; 32 states, 2048 channels: 418 against 415), except past 32 states, where a tile
+// holds fours of channels for half of them only (64 states, 2048 channels, four sequences: 989 us against 911 with half).
 template <bool BF16, int L>
 kda_status launch_scan_fwd(const kda::ScanParams &p, int64_t blocks, bool cut, cudaStream_t s) {
     if (cut) {
         const kda_status st = launch_scan_pass<BF16, L, 256, true>(p, blocks, s);
         if (st != KDA_OK) return st;
     }
-    return blocks >= 2 * (int64_t)device_sm_count() ? launch_scan_pass<BF16, L, 128, false>(p, blocks, s)
-                                                    : launch_scan_pass<BF16, L, 256, false>(p, blocks, s);
+    constexpr bool kPair = kda::ScanSmem<BF16, L, 128>::kPair;
+    if constexpr (!kPair && !kda::ScanSmem<BF16, L, 256>::kAllStage) {
+        return launch_scan_pass<BF16, L, 128, false>(p, blocks, s);
+    } else {
+        if constexpr (kPair)
+            if (blocks >= 2 * (int64_t)device_sm_count()) return launch_scan_pass<BF16, L, 128, false>(p, blocks, s);
+        return launch_scan_pass<BF16, L, 256, false>(p, blocks, s);
+    }
 }
 
 // the checks that the scan's entry points share; `where` names the entry point

@@ -11,7 +11,7 @@
 // channel) (softplus, the gate) is done once, not once per state.
 //   - A channel's n states lie on L = 2^ceil(log2(n / 4)) lanes, four to a lane; 128 threads scan
 //     KC x 128 / L channels of one group over one segment of one sequence.
-//   - 256 more threads (128 where two blocks share an SM) stage the next tile of tokens and write the
+//   - 256 more threads (or 128: launch_scan_fwd says where) stage the next tile of tokens and write the
 //     outputs of the last one meanwhile, so that the scanning warps only scan: with one sequence there is
 //     about one of them per scheduler.
 //   - What a scanning thread reads from shared memory per token is the next bound: B and C lie next to
@@ -201,6 +201,8 @@ __device__ __forceinline__ void decays(const float (&A2)[4], float delta, f32x2 
     a23 = f2_pack(ex2_approx(A2[2] * delta), ex2_approx(A2[3] * delta));
 }
 
+constexpr int kSmSharedBytes = 228 * 1024, kBlockReserve = 1024;   // an SM's shared memory, and what every block takes of it besides its own
+
 template <bool BF16, int L, int ST>
 struct ScanSmem {
     using Tile = ScanTile<L, ST>;
@@ -212,6 +214,8 @@ struct ScanSmem {
     static constexpr int kRaw = ST * (3 * Tile::kR * kFour + Tile::kQ * (int)sizeof(QuadBC<BF16>));   // of one tile on its way
     static constexpr int kStages = 3;
     static constexpr int kBytes = 2 * kBuf + kStages * kRaw;
+    static constexpr bool kPair = 2 * (kBytes + kBlockReserve) <= kSmSharedBytes;   // two blocks fit an SM
+    static constexpr bool kAllStage = Tile::kTT * Tile::kFR >= ST;                  // a tile's rows hold fours of channels for all
 };
 
 // Asynchronous copy of four elements to shared memory, or zeros past `on` of them; `unit`: how many elements (4, 2
@@ -266,9 +270,10 @@ __device__ __forceinline__ void raw_four(const void *p, float (&v)[4]) {
 // are written, tile i + 1 is converted and the tiles after it are on their way into a ring (every
 // staging thread reads back what it copied itself).
 template <bool BF16, int L, int ST, bool SUMMARY>
-__global__ void __launch_bounds__(kScanThreads + ST, ST == 128 ? 2 : 1) scan_fwd_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kScanThreads + ST, ST == 128 && ScanSmem<BF16, L, ST>::kPair ? 2 : 1) scan_fwd_kernel(const ScanParams p) {
     using Tile = ScanTile<L, ST>;
     using SM = ScanSmem<BF16, L, ST>;
+    static_assert(ST == 256 || SM::kPair || !ScanSmem<BF16, L, 256>::kAllStage, "fewer staging threads for nothing");
     constexpr int CH = Tile::kCH, TT = Tile::kTT, R = Tile::kR, Q = Tile::kQ, YS = Tile::kYS, FR = Tile::kFR, NS = SM::kStages;
     extern __shared__ __align__(16) unsigned char scan_tiles[];
     auto buf_bc = [&](int b) { return reinterpret_cast<QuadBC<BF16> *>(scan_tiles + b * SM::kBuf); };

@@ -1038,3 +1038,33 @@ def test_scan_without_skip_keeps_infinities(kda):
     # the output enters the gate's gradient: dz = dout y silu'(z)
     g = kda.kda_selective_scan_bwd(u, dt, A_log, BC, BC, dev_cu([T]), one(T, D), z=one(T, D))
     assert torch.isfinite(g["dz"][:at]).all() and (g["dz"][at:] == up).all()
+
+
+# ---- launch rules --------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D,n", [(8192, 4), (4096, 8), (4096, 16), (2048, 32), (1024, 64), (128, 64)])
+def test_scan_forward_where_blocks_could_share_an_sm(kda, D, n, t):
+    """More blocks than twice the SMs hold one each, in both types and for every number of lanes: in bf16 two share an
+    SM, in fp32 one has it alone.  (The last case: few blocks, where fp32 has half the staging threads too.)"""
+    lens = [90, 150, 0, 33, 70, 1]
+    v = scan_inputs(lens, D, 1, n, t)
+    args, kw = call_args(v)
+    out, last = kda.kda_selective_scan_fwd(*args, dev_cu(lens), **kw)
+    check_scan(kda, lens, v, out, last)
+
+
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+def test_scan_one_long_sequence_among_short_ones(kda, t):
+    """The channels of nine sequences nearly fill the GPU, so that nothing is cut, but one sequence has most of the tokens."""
+    lens, D, n = [24, 24, 24, 1500, 0, 24, 24, 24, 24], 512, 16
+    assert kda.kda_selective_scan_fwd_workspace_size(sum(lens), len(lens), D, n) == 0
+    v = scan_inputs(lens, D, 1, n, t)
+    args, kw = call_args(v)
+    cu = dev_cu(lens)
+    out, last = kda.kda_selective_scan_fwd(*args, cu, **kw)
+    check_scan(kda, lens, v, out, last)
+    dout = torch.randn(sum(lens), D, generator=gen(3), device="cuda").to(t)
+    dlast = torch.randn(len(lens), D, n, generator=gen(4), device="cuda")
+    check_scan_grads(lens, v, dout, dlast, kda.kda_selective_scan_bwd(*args, cu, dout, dfinal_state=dlast, **kw))
