@@ -147,10 +147,13 @@ struct ScanBwdSmem {
     static constexpr int kCkpt = Tile::kTC / Tile::kBack * kBackKC * 16 * kScanThreads;  // every kBack-th state
     static constexpr int kRed = 2 * (kScanThreads / 32) * Tile::kBack * 8 * L * 4;             // two buffers of the warps' dB, dC rows
     static constexpr int kGrad = kChunk + kCkpt + kRed;
+    // Blocks an SM that the kernels' registers are bounded for: no more than its shared memory holds.
+    static constexpr int at_most(int blocks, int bytes) { return blocks * (bytes + kBlockReserve) <= kSmSharedBytes ? blocks : at_most(blocks - 1, bytes); }
+    static constexpr int kChunkBlocks = at_most(L > 4 ? 3 : 5, kChunk), kGradBlocks = at_most(L > 4 ? 2 : 3, kGrad);
 };
 
 template <bool BF16, int L, bool VEC>
-__global__ void __launch_bounds__(kScanThreads, L > 4 ? 3 : 5) scan_bwd_chunk_kernel(const ScanBwdParams p) {
+__global__ void __launch_bounds__(kScanThreads, (ScanBwdSmem<BF16, L>::kChunkBlocks)) scan_bwd_chunk_kernel(const ScanBwdParams p) {
     using Tile = ScanBwdTile<L>;
     using SM = ScanBwdSmem<BF16, L>;
     constexpr int CH = Tile::kCH, YS = Tile::kYS, KC = kBackKC;
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(kChainThreads) scan_bwd_chain_kernel(const Sca
 }
 
 template <bool BF16, int L, bool VEC>
-__global__ void __launch_bounds__(kScanThreads, L > 4 ? 2 : 3) scan_bwd_grad_kernel(const ScanBwdParams p) {
+__global__ void __launch_bounds__(kScanThreads, (ScanBwdSmem<BF16, L>::kGradBlocks)) scan_bwd_grad_kernel(const ScanBwdParams p) {
     using Tile = ScanBwdTile<L>;
     using SM = ScanBwdSmem<BF16, L>;
     constexpr int TC = Tile::kTC, CH = Tile::kCH, YS = Tile::kYS, KC = kBackKC, kBack = Tile::kBack;
