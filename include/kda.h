@@ -352,7 +352,8 @@ KDA_API size_t kda_chunk_bwd_workspace_size(int64_t total_tokens, int32_t num_se
  * states need only their own type's alignment; where all of a call's are 16-byte aligned and rows hold
  * whole vectors, they are moved as vectors.  Workspaces are 16-byte aligned.  At most 2,147,418,112 tokens
  * a call, and 16,777,216 channels (D, or H d) in the scan and the convolution.  No output (nor workspace) of a call
- * overlaps an input or another output, but for states updated in place where that is said.
+ * overlaps an input or another output, but for states updated in place where that is said.  Infinities and NaN reach only
+ * what depends on them by the formulas; where those give an infinity, the scan may give NaN.
  *
  * Selective state space scan: the recurrence of a state-space layer, beside the gated delta rule.  Per channel c of D with n states, in group g = c / (D / G):
  *   delta_t = softplus(dt_t + dt_bias),  A = -exp(A_log)

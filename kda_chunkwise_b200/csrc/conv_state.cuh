@@ -5,12 +5,11 @@
 //   s = silu(p) or p;   y = s, or s / sqrt(|s|^2 + 1e-12) over the head's channels
 // The carried state is the last W - 1 inputs, [num_seqs, W - 1, C] in the inputs' type, oldest first.
 //
-// All three are bound by memory (about 10 flops a byte at most): each input is read once, its
-// neighbours in time come from registers, and a thread keeps several rows in flight, in a ring in shared
-// memory that it alone reads.  A thread owns E channels, laid out as ConvCols says; where they are not moved as
-// vectors, a batch of rows is in registers instead.  8192 x 4096 channels, W = 4, SiLU and unit rows, bf16: forward
-// 38 us (134 MB, 3.6 TB/s), backward 75 us + 6 for the weights' sums (201 MB, 2.7 TB/s).  Both are held by
-// instructions more than by memory: 44 % and 53 % of the issue slots busy at four blocks an SM.
+// About 10 flops a byte at most, so each input is read once, its neighbours in time come from registers, and a
+// thread keeps several rows in flight, in a ring in shared memory that it alone reads.  A thread owns E channels, laid
+// out as ConvCols says; where they are not moved as vectors, a batch of rows is in registers instead.  8192 x 4096 channels, W = 4, SiLU and unit rows, bf16: forward
+// 38 us (134 MB, 3.6 TB/s), backward 75 us + 6 for the weights' sums (201 MB, 2.7 TB/s).  Neither reaches memory's
+// rate: the instructions and their latency hold them, 44 % and 53 % of the issue slots busy at four blocks an SM.
 #pragma once
 
 #include <type_traits>

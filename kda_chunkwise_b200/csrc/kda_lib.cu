@@ -1311,7 +1311,8 @@ bool scan_sizes_ok(int64_t rows, int32_t seqs, int32_t D, int32_t n, int32_t G) 
 // an empty sequence at the very end has its record too).  A block takes an SM, so cutting pays where at least
 // two segments of every sequence run side by side (it takes their exponentials twice): as many as fill the SMs
 // once, of two tiles or more.  8192 tokens x 16 states, uncut against cut: 256 channels 290 and 47 us
-// (16 segments), 1024 channels 297 and 141 (4), 2048 channels 307 and 274 (2).
+// (16 segments), 1024 channels 297 and 141 (4), 2048 channels 307 and 274 (2).  Sequences count alike whatever their
+// lengths: one long one among short ones that fill the GPU's blocks is not cut.
 int64_t scan_segment_len(int64_t T, int32_t num_seqs, int32_t D, int32_t n, int32_t G) {
     const int64_t blocks = (int64_t)G * scan_blocks_of_group(D, n, G, 1);
     const int64_t each = device_sm_count() / (blocks * num_seqs);

@@ -8,8 +8,9 @@
 // of each in a thread's registers, so that a row is read once and its statistics are taken in two passes
 // (the mean first: no difference of large sums).  The next rows are on their way into a ring in shared
 // memory meanwhile, 16 bytes a copy, every thread reading back its own; the weights stay in registers.
-// 8192 x 4096 in bf16: forward 25 us (134 MB, 5.4 TB/s, 0.82 of a copy), backward 43 us + 9 for the weights' sums,
-// cold (201 MB, 4.7 TB/s, 0.71; two blocks an SM, one barrier a row).
+// 8192 x 4096 in bf16: forward 25 us (134 MB, 5.4 TB/s, 0.82 of a copy), backward 43 to 45 us + 9 for the weights'
+// sums, cold (201 MB, 4.5 to 4.7 TB/s, 0.68 to 0.71; two blocks an SM, one barrier a row).  Its registers do not hold everything of wide
+// rows: 200 to 304 bytes a thread are spilled above 8192 columns, up to 24 in fp32 at 1025 to 4096 and in bf16 at 4097 to 8192.
 // Backwards each group keeps its columns' shares of dw and db in registers and leaves one row of
 // partial sums; a second launch adds those in a fixed order.
 #pragma once

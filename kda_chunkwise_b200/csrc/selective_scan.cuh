@@ -10,19 +10,19 @@
 // computed twice that takes an exponential, states stay in registers, and what is per (token,
 // channel) (softplus, the gate) is done once, not once per state.
 //   - A channel's n states lie on L = 2^ceil(log2(n / 4)) lanes, four to a lane; 128 threads scan
-//     KC x 128 / L channels of one group over one segment of one sequence.
+//     128 / L channels of one group over one segment of one sequence.
 //   - 256 more threads (or 128: launch_scan_fwd says where) stage the next tile of tokens and write the
 //     outputs of the last one meanwhile, so that the scanning warps only scan: with one sequence there is
 //     about one of them per scheduler.
 //   - What a scanning thread reads from shared memory per token is the next bound: B and C lie next to
-//     each other, in bf16 where they came in bf16, and serve the KC channels of a thread.
+//     each other, in bf16 where they came in bf16, so that four states of both are one load.
 //   - The sum over the states is taken for L tokens at once (transposed_sums): one value a lane.
 // 8192 tokens x 4096 channels x 16 states in bf16 take 297 us; the states' exponentials alone would take 119.
 // At 2048 tokens the exponential unit is 56 %, the issue slots 51 % and the shared-memory data path 46 % busy, with
 // four scanning and eight staging warps an SM.  Two states a lane, so twice the scanning warps, took
 // 300 us against 306 without the call around it: 2 %, not taken.
-// Sequences longer than seg_len tokens are cut into segments where the channels alone would leave
-// the GPU empty: a first launch finds every segment's end state from zero and its sum of delta (the
+// Sequences longer than seg_len tokens are cut into segments where the channels of all sequences together would leave
+// the GPU half empty (scan_segment_len; one long sequence among short ones is therefore not cut): a first launch finds every segment's end state from zero and its sum of delta (the
 // decay over a segment is exp(A sum delta)), the second joins those before its own and scans.
 #pragma once
 
@@ -556,9 +556,9 @@ constexpr int kScanStepThreads = 256;
 
 // One token of N states: the state is read once and written once (0.9 flop a byte), so the kernel
 // streams it.  A thread owns four states of one channel (16 bytes) and walks over rows of the batch, the
-// decay's weights read once for all its rows.  Few registers, so that many warps hide the loads, do
-// better than a row in advance or several rows at once (29 us against 33 and 37 at 256 rows of 4096
-// channels and 16 states, 143 MB).
+// decay's weights read once for all its rows.  256 rows of 4096 channels and 16 states (143 MB) take 36 us a call,
+// 4.0 TB/s.  Few registers, so that many warps hide the loads, do better than a row in advance or several rows at once
+// (29 us against 33 and 37 with the kernel alone repeated, part of the state then in the L2).
 template <bool BF16, int L, bool VEC>
 __global__ void __launch_bounds__(kScanStepThreads) scan_step_kernel(const ScanStepParams p) {
     const int64_t q = (int64_t)blockIdx.x * kScanStepThreads + threadIdx.x;   // quad of a row of the batch

@@ -19,7 +19,7 @@
 //                             du, ddt and the output take the places of u, delta and dy
 //   4. two sums of partial results over channel blocks (dB, dC) and over chunks (the weights)
 // Under three exponentials per (token, channel, state); sums are taken in a fixed order, so results do not
-// vary between runs.  8192 tokens x 4096 channels x 16 states in bf16: 249 + 51 + 801 + 15 + 20 us, cold.
+// vary between runs.  8192 tokens x 4096 channels x 16 states in bf16: 249 + 51 + 794 + 15 + 20 us, cold.
 // At 2048 tokens the chunk kernel has the exponential unit 62 % and the issue slots 68 % busy, the gradient kernel
 // the slots 59 % and the shared-memory data path 44 % (three blocks an SM: 168 registers, 66 KB); the chain moves
 // 268 MB.  Taken out one at a time, the sums of dB and dC over a warp's channels save 121 us of the gradient
