@@ -1068,3 +1068,17 @@ def test_scan_one_long_sequence_among_short_ones(kda, t):
     dout = torch.randn(sum(lens), D, generator=gen(3), device="cuda").to(t)
     dlast = torch.randn(len(lens), D, n, generator=gen(4), device="cuda")
     check_scan_grads(lens, v, dout, dlast, kda.kda_selective_scan_bwd(*args, cu, dout, dfinal_state=dlast, **kw))
+
+
+@pytest.mark.parametrize("t", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D,n", [(9, 33), (24, 64)])
+def test_scan_forward_cut_past_32_states(kda, D, n, t):
+    """Both passes over segments, which stage with different numbers of threads in fp32; the final states in place."""
+    lens = [700, 0, 1, 300]
+    assert kda.kda_selective_scan_fwd_workspace_size(sum(lens), len(lens), D, n) > 0
+    v = scan_inputs(lens, D, 1, n, t)
+    args, kw = call_args(v)
+    pool = v["h0"].clone()
+    out, last = kda.kda_selective_scan_fwd(*args, dev_cu(lens), **{**kw, "initial_state": pool}, final_state=pool)
+    assert last is pool
+    check_scan(kda, lens, v, out, last)
